@@ -15,11 +15,19 @@ from .binding import (  # noqa: F401
     OP_EXPAND,
     OP_FUSED,
     OP_SHRINK,
+    Q8Rows,
+    Q8Weights,
     load,
+    new_q8_rows,
+    new_q8_weights,
     new_workspace,
     new_workspace_graph,
     new_workspace_multi,
     packed_backward,
+    packed_backward_q8,
+    q8_dequantize,
+    q8_matmul,
+    q8_quantize,
     segments_from_ids,
     sgmv_expand,
     sgmv_fused,
@@ -27,6 +35,8 @@ from .binding import (  # noqa: F401
     sgmv_fused_multi,
     sgmv_fused_noalloc,
     sgmv_shrink,
+    swiglu,
+    swiglu_backward,
     version,
     workspace_size,
     workspace_size_graph,

@@ -52,10 +52,17 @@ class CGraphAdapters(ctypes.Structure):
                 ("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class CQ8(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("ld", ctypes.c_int64), ("exps", ctypes.c_void_p),
+                ("ld_exps", ctypes.c_int64), ("rows", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("block_rows", ctypes.c_int32)]
+
+
 EXPORTS = ["lora_segments_from_ids", "lora_workspace_size", "lora_sgmv_shrink", "lora_sgmv_expand",
            "lora_sgmv_fused", "lora_packed_backward", "lora_workspace_size_multi",
            "lora_sgmv_fused_multi", "lora_sgmv_fused_noalloc", "lora_workspace_size_graph",
-           "lora_sgmv_fused_graph", "lora_status_string", "lora_last_error", "lora_version"]
+           "lora_sgmv_fused_graph", "lora_q8_quantize", "lora_q8_dequantize", "lora_q8_matmul",
+           "lora_packed_backward_q8", "lora_swiglu", "lora_swiglu_backward", "lora_status_string", "lora_last_error", "lora_version"]
 NOALLOC_SCRATCH_BYTES = 16 << 20  # LORA_NOALLOC_SCRATCH_BYTES
 
 _lib = None
@@ -97,6 +104,14 @@ def load(path: str = LIB_PATH):
                                               ctypes.POINTER(ctypes.c_size_t)]
     lib.lora_sgmv_fused_graph.argtypes = [P, I64, ctypes.POINTER(CGraphAdapters), P, ctypes.c_int32, P, I64,
                                           P, ctypes.c_size_t, P]
+    Q = ctypes.POINTER(CQ8)
+    lib.lora_q8_quantize.argtypes = [P, I64, Q, Q, P]
+    lib.lora_q8_dequantize.argtypes = [Q, P, I64, P]
+    lib.lora_q8_matmul.argtypes = [Q, Q, P, I64, ctypes.c_uint32, P]
+    lib.lora_packed_backward_q8.argtypes = [Q, P, I64, P, I64, ctypes.POINTER(CAdapters), ctypes.POINTER(CSegments),
+                                            P, I64, P, P, ctypes.c_uint32, P, ctypes.c_size_t, P]
+    lib.lora_swiglu.argtypes = [P, I64, ctypes.c_int32, ctypes.c_int32, P, I64, Q, P]
+    lib.lora_swiglu_backward.argtypes = [P, I64, P, I64, ctypes.c_int32, ctypes.c_int32, P, I64, Q, P]
     lib.lora_status_string.restype = ctypes.c_char_p
     lib.lora_status_string.argtypes = [ctypes.c_int]
     lib.lora_last_error.restype = ctypes.c_char_p
@@ -368,6 +383,152 @@ def sgmv_fused_multi(x, adapters: Sequence[Adapters], segments: Segments, ys: Se
     _check(lib.lora_sgmv_fused_multi(_ptr(x), x.stride(0), len(adapters), ctypes.cast(arr, ctypes.c_void_p),
                                      segments.c, ctypes.cast(yp, ctypes.c_void_p),
                                      ctypes.cast(ld, ctypes.c_void_p), wp, wb, _stream_handle(stream)))
+
+
+# ---------------------------------------------------------------------------
+# 8-bit rows and weights, the frozen projection, the gated activation
+# ---------------------------------------------------------------------------
+class _Q8:
+    """A matrix in 8 bits: e4m3 values [rows, >= 128 * ceil(width / 128)] and
+    biased power-of-two exponents, one per 128 columns of `block_rows` rows."""
+
+    block_rows = 1
+
+    def __init__(self, values, exps, width: int, rows: Optional[int] = None):
+        import torch
+        if values.dtype not in (torch.uint8, torch.float8_e4m3fn) or values.dim() != 2 or values.stride(1) != 1:
+            raise ValueError("values must be a 2-D uint8 or float8_e4m3fn tensor with unit column stride")
+        if exps.dtype != torch.uint8 or exps.dim() != 2 or exps.stride(1) != 1:
+            raise ValueError("exps must be a 2-D uint8 tensor with unit column stride")
+        self.rows = int(values.shape[0] if rows is None else rows)
+        self.width = int(width)
+        blocks, erows = -(-self.width // 128), -(-self.rows // self.block_rows)
+        if self.rows < 0 or self.rows > values.shape[0] or values.shape[1] < 128 * blocks:
+            raise ValueError(f"values of shape {tuple(values.shape)} do not hold {self.rows} rows of {128 * blocks} bytes")
+        # whole dwords of exponents: the products read four blocks at a time
+        if exps.shape[0] < erows or exps.stride(0) < -(-blocks // 4) * 4 or exps.shape[1] < blocks:
+            raise ValueError(f"exps of shape {tuple(exps.shape)} do not hold {erows} rows of {blocks} blocks "
+                             "with a stride that is a multiple of 4")
+        if values.device != exps.device:
+            raise ValueError(f"values are on {values.device}, exps on {exps.device}")
+        self.values, self.exps = values, exps
+        self._c = CQ8(_ptr(values), values.stride(0), _ptr(exps), exps.stride(0), self.rows, self.width,
+                      self.block_rows)
+
+    @property
+    def c(self):
+        return ctypes.byref(self._c)
+
+    @property
+    def device(self):
+        return self.values.device
+
+
+class Q8Rows(_Q8):
+    """8-bit rows (activations, checkpoints): one scale per row and 128 columns."""
+
+
+class Q8Weights(_Q8):
+    """8-bit weights [h_out, h_in]: one scale per 128 x 128 block."""
+
+    block_rows = 128
+
+
+def _new_q8(cls, rows: int, width: int, device):
+    import torch
+    blocks, erows = -(-int(width) // 128), -(-int(rows) // cls.block_rows)
+    v = torch.empty((int(rows), 128 * blocks), dtype=torch.uint8, device=device)
+    e = torch.empty((erows, -(-blocks // 4) * 4), dtype=torch.uint8, device=device)
+    return cls(v, e, width)
+
+
+def new_q8_rows(rows: int, width: int, device="cuda") -> Q8Rows:
+    return _new_q8(Q8Rows, rows, width, device)
+
+
+def new_q8_weights(rows: int, width: int, device="cuda") -> Q8Weights:
+    return _new_q8(Q8Weights, rows, width, device)
+
+
+def _rows_arg(name: str, t, rows: int, width: int, device):
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.stride(1) != 1 or t.shape[0] < rows or t.shape[1] != width:
+        raise ValueError(f"{name} must be a bfloat16 [>= {rows}, {width}] matrix with unit column stride, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _call_on(device, stream, fn, *args):
+    """Calls fn(*args, stream) with `device` current, on `stream` or the
+    device's current stream."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"device tensors are needed, got {device}")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _check(fn(*args, _stream_handle(stream)))
+    _check(fn(*args, _stream_handle(stream)))
+
+
+def q8_quantize(x, out: _Q8, out_t: Optional[Q8Weights] = None, stream=None):
+    """Stores bf16 x in 8 bits (Q8Rows or Q8Weights); with out_t the
+    transposed weights too."""
+    _rows_arg("x", x, out.rows, out.width, out.device)
+    if out_t is not None and out_t.device != out.device:
+        raise ValueError(f"out_t is on {out_t.device}, expected {out.device}")
+    _call_on(out.device, stream, load().lora_q8_quantize, _ptr(x), x.stride(0), out.c,
+             out_t.c if out_t is not None else None)
+
+
+def q8_dequantize(q: _Q8, x, stream=None):
+    """Restores an 8-bit matrix to bf16 x."""
+    _rows_arg("x", x, q.rows, q.width, q.device)
+    _call_on(q.device, stream, load().lora_q8_dequantize, q.c, _ptr(x), x.stride(0))
+
+
+def q8_matmul(x: Q8Rows, w: Q8Weights, y, accumulate: bool = False, stream=None):
+    """y = x w^T (or y += x w^T) on 8-bit operands; y bf16 [x.rows, w.rows]."""
+    _rows_arg("y", y, x.rows, w.rows, x.device)
+    if w.device != x.device:
+        raise ValueError(f"w is on {w.device}, expected {x.device}")
+    _call_on(x.device, stream, load().lora_q8_matmul, x.c, w.c, _ptr(y), y.stride(0), 1 if accumulate else 0)
+
+
+def packed_backward_q8(x: Q8Rows, dy, u, adapters: Adapters, segments: Segments, dx, dA_ptrs, dB_ptrs,
+                       flags: int = 0, ws=None, stream=None):
+    """packed_backward with x as the 8-bit checkpoint; u (the forward's
+    u_save) is required."""
+    wp, wb = _ws(ws)
+    _call_on(x.device, stream, load().lora_packed_backward_q8, x.c, _ptr(dy), dy.stride(0) if dy is not None else 0,
+             _ptr(u), u.stride(0) if u is not None else 0, adapters.c, segments.c, _ptr(dx),
+             dx.stride(0) if dx is not None else 0, _ptr(dA_ptrs), _ptr(dB_ptrs), int(flags), wp, wb)
+
+
+def swiglu(gate_up, h=None, hq: Optional[Q8Rows] = None, stream=None):
+    """h = silu(gate) * up of gate_up [T, 2F], as bf16 rows and/or 8-bit rows."""
+    T, F = int(gate_up.shape[0]), int(gate_up.shape[1]) // 2
+    _rows_arg("gate_up", gate_up, T, 2 * F, gate_up.device)
+    if h is not None:
+        _rows_arg("h", h, T, F, gate_up.device)
+    if hq is not None and hq.device != gate_up.device:
+        raise ValueError(f"hq is on {hq.device}, expected {gate_up.device}")
+    _call_on(gate_up.device, stream, load().lora_swiglu, _ptr(gate_up), gate_up.stride(0), T, F, _ptr(h),
+             h.stride(0) if h is not None else 0, hq.c if hq is not None else None)
+
+
+def swiglu_backward(gate_up, dh, dgate_up=None, dgate_up_q: Optional[Q8Rows] = None, stream=None):
+    """The gradient of swiglu's input, [T, 2F], as bf16 rows and/or 8-bit rows."""
+    T, F = int(gate_up.shape[0]), int(gate_up.shape[1]) // 2
+    _rows_arg("gate_up", gate_up, T, 2 * F, gate_up.device)
+    _rows_arg("dh", dh, T, F, gate_up.device)
+    if dgate_up is not None:
+        _rows_arg("dgate_up", dgate_up, T, 2 * F, gate_up.device)
+    if dgate_up_q is not None and dgate_up_q.device != gate_up.device:
+        raise ValueError(f"dgate_up_q is on {dgate_up_q.device}, expected {gate_up.device}")
+    _call_on(gate_up.device, stream, load().lora_swiglu_backward, _ptr(gate_up), gate_up.stride(0), _ptr(dh),
+             dh.stride(0), T, F, _ptr(dgate_up), dgate_up.stride(0) if dgate_up is not None else 0,
+             dgate_up_q.c if dgate_up_q is not None else None)
 
 
 class CPlanItem(ctypes.Structure):

@@ -20,6 +20,7 @@
 #include "lora_inspect.h"
 #include "lora_internal.h"
 #include "lora_plan.h"
+#include "lora_q8.h"
 
 namespace lora {
 hipError_t launch_fwd(const FwdPlan& P, int rbmax, hipStream_t stream, const uint64_t* wptr,
@@ -91,6 +92,11 @@ DeviceInfo device_info() {
 struct Launcher {
   virtual ~Launcher() = default;
   virtual DeviceInfo dev() = 0;
+  // whether the stream is being captured into a HIP graph
+  virtual hipError_t capturing(bool& is) {
+    is = false;
+    return hipSuccess;
+  }
   // rows (host, n_rows entries) or null: the token-row table a small launch
   // carries in its arguments
   virtual hipError_t fwd(const FwdPlan& P, int rbmax, const uint64_t* wptr, const uint64_t* vptr,
@@ -105,6 +111,12 @@ struct HipLauncher final : Launcher {
   hipStream_t stream;
   explicit HipLauncher(void* s) : stream(static_cast<hipStream_t>(s)) {}
   DeviceInfo dev() override { return device_info(); }
+  hipError_t capturing(bool& is) override {
+    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+    const hipError_t e = hipStreamIsCapturing(stream, &st);
+    is = st != hipStreamCaptureStatusNone;
+    return e;
+  }
   hipError_t fwd(const FwdPlan& P, int rbmax, const uint64_t* wptr, const uint64_t* vptr, const int32_t* rows,
                  int n_rows) override {
     return launch_fwd(P, rbmax, stream, wptr, vptr, rows, n_rows);
@@ -1041,9 +1053,17 @@ static int packed_backward_impl(const void* x, int64_t ldx, const void* dy, int6
                                 int64_t ldu, const lora_adapters_t* adapters,
                                 const lora_segments_t* segments, void* dx, int64_t lddx,
                                 const uint64_t* dA_ptrs, const uint64_t* dB_ptrs, uint32_t flags,
-                                void* ws, size_t ws_bytes, Launcher& launcher) {
+                                void* ws, size_t ws_bytes, Launcher& launcher, const lora_q8_t* x8 = nullptr) {
   int st = common_checks(adapters, segments);
   if (st) return st;
+  if (x8) {
+    if ((st = check_q8(x8, "x", 1))) return st;
+    if (x8->width != adapters->h_in)
+      return fail(LORA_INVALID_ARGUMENT, "x is %d wide, h_in is %d", x8->width, adapters->h_in);
+    // its rows are addressed like every other matrix of the call
+    if (x8->ld > kGatherSpan / 64 || x8->ld_exps > kGatherSpan / 64)
+      return fail(LORA_UNSUPPORTED, "row strides of x above %lld bytes are not supported", (long long)(kGatherSpan / 64));
+  }
   if (flags & ~LORA_GRAD_ACCUMULATE) return fail(LORA_INVALID_ARGUMENT, "unknown flags 0x%x", flags);
   const bool accumulate = (flags & LORA_GRAD_ACCUMULATE) != 0;
   const int N = adapters->num_adapters;
@@ -1058,10 +1078,18 @@ static int packed_backward_impl(const void* x, int64_t ldx, const void* dy, int6
   if (segs.empty() && !any_zero_fill) return LORA_OK;
   if (!dA_ptrs || !dB_ptrs) return fail(LORA_INVALID_ARGUMENT, "dA_ptrs/dB_ptrs is NULL");
   if (!segs.empty()) {
-    if ((st = check_rows(x, ldx, adapters->h_in, "x", true))) return st;
+    if ((st = check_rows(x, ldx, adapters->h_in, "x", !x8))) return st;
     if ((st = check_rows(dy, lddy, adapters->h_out, "dy", true))) return st;
     if ((st = check_rows(dx, lddx, adapters->h_in, "dx", dx != nullptr))) return st;
-    if ((st = check_gather(segments, ldx, adapters->h_in, "x", true))) return st;
+    if ((st = check_gather(segments, ldx, adapters->h_in, "x", !x8))) return st;
+    if (x8) {
+      if (!u) return fail(LORA_INVALID_ARGUMENT, "u is NULL: the backward of a checkpoint needs the forward's u");
+      if (x8->rows < segments->num_tokens)
+        return fail(LORA_INVALID_ARGUMENT, "x has %d rows, the batch %d tokens", x8->rows, segments->num_tokens);
+      if (segments->token_rows && (int64_t)(segments->num_tokens - 1) * x8->ld + x8->width > kGatherSpan)
+        return fail(LORA_INVALID_ARGUMENT, "x: with token_rows, %d rows of stride %lld are above the %lld-byte gather limit",
+                    segments->num_tokens, (long long)x8->ld, (long long)kGatherSpan);
+    }
     if ((st = check_gather(segments, lddy, adapters->h_out, "dy", true))) return st;
     if ((st = check_gather(segments, lddx, adapters->h_in, "dx", dx != nullptr))) return st;
     if (segments->token_rows_host && !segments->token_rows)
@@ -1071,6 +1099,13 @@ static int packed_backward_impl(const void* x, int64_t ldx, const void* dy, int6
   }
   const WsLayout L = ws_layout(LORA_OP_BACKWARD, adapters, segments);
   if ((st = check_ws(ws, ws_bytes, L.total))) return st;
+  if (x8) {
+    bool captured = false;
+    const hipError_t e = launcher.capturing(captured);
+    if (e != hipSuccess) return fail(LORA_DEVICE_ERROR, "hipStreamIsCapturing failed: %s", hipGetErrorString(e));
+    if (captured)
+      return fail(LORA_INVALID_ARGUMENT, "the stream is being captured: the launches' hand-off ids cannot be replayed");
+  }
 
   char* wsb = static_cast<char*>(ws);
   float* partials = reinterpret_cast<float*>(wsb + L.partials);
@@ -1224,6 +1259,11 @@ static int packed_backward_impl(const void* x, int64_t ldx, const void* dy, int6
       WgradPlan W;
       std::memset(&W, 0, sizeof(W));
       W.x = static_cast<const uint16_t*>(x); W.ldx = ldx;
+      if (x8) {
+        W.x8 = x8->values; W.ldx8 = x8->ld;
+        W.x8_exps = x8->exps; W.ldx8_exps = x8->ld_exps;
+        W.x8_rows = x8->rows;
+      }
       W.dy = static_cast<const uint16_t*>(dy); W.lddy = lddy;
       W.U = Uuse; W.ldu = lduse; W.dU = dU; W.lddu = L.lddu;
       W.dA_tab = dA_ptrs; W.dB_tab = dB_ptrs; W.token_rows = segments->token_rows;
@@ -1389,6 +1429,21 @@ int lora_packed_backward(const void* x, int64_t ldx, const void* dy, int64_t ldd
   HipLauncher launcher(stream);
   return packed_backward_impl(x, ldx, dy, lddy, u, ldu, adapters, segments, dx, lddx, dA_ptrs, dB_ptrs, flags,
                               ws, ws_bytes, launcher);
+}
+
+int lora_packed_backward_q8(const lora_q8_t* x, const void* dy, int64_t lddy, const float* u, int64_t ldu,
+                            const lora_adapters_t* adapters, const lora_segments_t* segments, void* dx,
+                            int64_t lddx, const uint64_t* dA_ptrs, const uint64_t* dB_ptrs, uint32_t flags,
+                            void* ws, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  if (!x) return fail(LORA_INVALID_ARGUMENT, "x is NULL");
+  try {
+    HipLauncher launcher(stream);
+    return packed_backward_impl(nullptr, 0, dy, lddy, u, ldu, adapters, segments, dx, lddx, dA_ptrs, dB_ptrs, flags,
+                                ws, ws_bytes, launcher, x);
+  } catch (const std::exception& e) {  // host memory for the plan
+    return fail(LORA_DEVICE_ERROR, "planning failed: %s", e.what());
+  }
 }
 
 }  // extern "C"

@@ -7,8 +7,11 @@
 // walks all of that adapter's tokens, so the reduction is deterministic and
 // needs no atomics; tiles follow the hidden dimension, not the rank
 // ("Technische Samenvatting: PLoRA" (gist.science), "Kernelontwerp").
+#include <type_traits>
+
 #include "lora_device.h"
 #include "lora_plan.h"
+#include "lora_q8.h"
 
 namespace lora {
 
@@ -120,6 +123,18 @@ struct WgRegs {
   float q[2 * KB];        // this thread's share of the step's Q tile
 };
 
+// An 8-bit Z (dA from a checkpoint): the same rows and columns as e4m3
+// bytes, and one exponent byte per token and 128 columns. An item's columns
+// (256 for QN = 4, 128 for QN = 2) are whole blocks and a wave's lie in one of
+// them, so thread i < 32 * blocks loads the byte of block i / 32, token i % 32,
+// and the step's scales go through LDS beside its Q tile.
+template <int KB, int QN>
+struct WgRegs8 {
+  uint32_t z[8];    // QN bytes each
+  uint32_t e;       // this thread's exponent byte
+  float q[2 * KB];
+};
+
 __device__ __forceinline__ void wg_advance(const WgradPlan& P, int seg_end, WgCursor& c) {
   c.t0 += 32;
   while (c.t0 >= c.tend && c.seg < seg_end) {
@@ -183,8 +198,57 @@ __device__ __forceinline__ void wg_load(const WgradPlan& P, const uint16_t* Z, i
   }
 }
 
-template <int KB, int QN>
-__device__ __forceinline__ void wg_commit_q(const WgRegs<KB, QN>& R, float (*Qt)[kQtLd]) {
+// wg_load for an 8-bit Z. A row outside the checkpoint reads as zero.
+template <int KB, int QN, bool GATHER>
+__device__ __forceinline__ void wg_load8(const WgradPlan& P, const float* Q, int64_t ldq, int rank, int ccol,
+                                         bool col_ok, int col0, int seg_end, const WgCursor& c,
+                                         WgRegs8<KB, QN>& R) {
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  const bool live = c.seg < seg_end;
+  const int cnt = live ? min(32, c.tend - c.t0) : 0;
+  const int blocks = (P.h_in + kQ8Block - 1) / kQ8Block;
+  const int eb = (col0 >> 7) + (int)(threadIdx.x >> 5), et = threadIdx.x & 31;
+  const bool e_ok = (int)threadIdx.x < QN * 16 && eb < blocks && et < cnt;
+  __amdgpu_buffer_rsrc_t zr, er, rr;
+  if constexpr (GATHER) {
+    zr = mk_rsrc(P.x8, cnt > 0 ? kGatherSpan : 0);
+    er = mk_rsrc(P.x8_exps, cnt > 0 ? kGatherSpan : 0);
+    rr = mk_rsrc(P.token_rows + (live ? c.t0 : 0), (int64_t)cnt * 4);
+  } else {
+    const int64_t t0 = live ? c.t0 : 0;
+    zr = mk_rsrc(P.x8 + t0 * P.ldx8, cnt > 0 ? (int64_t)(cnt - 1) * P.ldx8 + P.h_in : 0);
+    er = mk_rsrc(P.x8_exps + t0 * P.ldx8_exps, cnt > 0 ? (int64_t)(cnt - 1) * P.ldx8_exps + blocks : 0);
+  }
+  // byte offset of column `col` of the step's row r in a matrix of stride ld
+  auto place = [&](int r, int64_t ld, int col, int bytes, bool ok) -> uint32_t {
+    int64_t row_bytes = (int64_t)r * ld;
+    if constexpr (GATHER) {
+      const int32_t row = (int32_t)__builtin_amdgcn_raw_buffer_load_b32(rr, ok ? 4 * r : (int)kOff, 0, 0);
+      row_bytes = (int64_t)row * ld;
+      ok = ok && row >= 0 && row < P.x8_rows && row_bytes <= kGatherSpan - bytes;
+    }
+    return ok ? (uint32_t)(row_bytes + col) : kOff;
+  };
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int r = 8 * g + e;
+    const uint32_t off = place(r, P.ldx8, ccol, P.h_in, col_ok && r < cnt);
+    if constexpr (QN == 4) R.z[e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(zr, (int)off, 0, kNT);
+    else R.z[e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(zr, (int)off, 0, kNT);
+  }
+  R.e = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(er, (int)place(et, P.ldx8_exps, eb, blocks, e_ok), 0, 0);
+  const __amdgpu_buffer_rsrc_t qr = mk_rsrc(Q + (int64_t)(live ? c.t0 : 0) * ldq, (int64_t)cnt * ldq * 4);
+#pragma unroll
+  for (int j = 0; j < 2 * KB; ++j) {
+    const int e2 = threadIdx.x + kThreads * j;
+    const int tt = e2 / (16 * KB), k = e2 - tt * (16 * KB);
+    const uint32_t off = (tt < cnt && k < rank) ? (uint32_t)(((int64_t)tt * ldq + k) * 4) : kOff;
+    R.q[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(qr, (int)off, 0, 0));
+  }
+}
+
+template <int KB, class Regs>
+__device__ __forceinline__ void wg_commit_q(const Regs& R, float (*Qt)[kQtLd]) {
 #pragma unroll
   for (int j = 0; j < 2 * KB; ++j) {
     const int e2 = threadIdx.x + kThreads * j;
@@ -193,21 +257,27 @@ __device__ __forceinline__ void wg_commit_q(const WgRegs<KB, QN>& R, float (*Qt)
   }
 }
 
-template <int KB, int QN>
-__device__ __forceinline__ void wg_compute(const WgRegs<KB, QN>& R, float (*Qt)[kQtLd], f32x4 (&acc)[QN][KB]) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, cl = lane & 15;
-  // A operand: frag q = Z[8g + e][column q], e = 0..7 (register transpose)
-  bf16x8 fa[QN];
+// A operand: frag q = Z[8g + e][column q], e = 0..7, from Z as bf16 pairs of
+// columns (register transpose)
+template <int QN>
+__device__ __forceinline__ void wg_transpose(const uint32_t (&z)[8][QN / 2], bf16x8 (&fa)[QN]) {
 #pragma unroll
   for (int q = 0; q < QN; ++q) {
     u32x4 v;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      const uint32_t lo = R.z[2 * d][q >> 1], hi = R.z[2 * d + 1][q >> 1];
+      const uint32_t lo = z[2 * d][q >> 1], hi = z[2 * d + 1][q >> 1];
       v[d] = (q & 1) ? ((lo >> 16) | (hi & 0xffff0000u)) : ((lo & 0xffffu) | (hi << 16));
     }
     fa[q] = as_bf16x8(v);
   }
+}
+
+// acc += Z^T Q of one step. EXACT: the fp32 Q enters as three bf16 parts
+// (24 mantissa bits) instead of two (16).
+template <int KB, int QN, bool EXACT>
+__device__ __forceinline__ void wg_compute(const bf16x8 (&fa)[QN], float (*Qt)[kQtLd], f32x4 (&acc)[QN][KB]) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, cl = lane & 15;
   // B operand: Q[8g + e][16kb + cl] as bf16 hi + lo
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
@@ -219,19 +289,22 @@ __device__ __forceinline__ void wg_compute(const WgRegs<KB, QN>& R, float (*Qt)[
       f[e] = q0[e];
       f[4 + e] = q1[e];
     }
-    bf16x8 qh, ql;
-    split8(f, qh, ql);
+    bf16x8 qh, ql, qx;
+    if constexpr (EXACT) split8(f, qh, ql, qx);
+    else split8(f, qh, ql);
 #pragma unroll
     for (int q = 0; q < QN; ++q) {
       acc[q][kb] = mfma16(fa[q], qh, acc[q][kb]);
       acc[q][kb] = mfma16(fa[q], ql, acc[q][kb]);
+      if constexpr (EXACT) acc[q][kb] = mfma16(fa[q], qx, acc[q][kb]);
     }
   }
 }
 
-template <int KB, int QN, bool GATHER>
+// Z8: Z is the 8-bit checkpoint (dA only). EXACT: see wg_compute.
+template <int KB, int QN, bool GATHER, bool Z8, bool EXACT>
 __device__ __forceinline__ void wgrad_item(const WgradPlan& P, int job, int kind, int chunk,
-                                           float (*Qt)[128][kQtLd]) {
+                                           float (*Qt)[128][kQtLd], float (*Es)[2][32]) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int g = lane >> 4, cl = lane & 15;
   const int a = P.job_adapter[job];
@@ -277,20 +350,43 @@ __device__ __forceinline__ void wgrad_item(const WgradPlan& P, int job, int kind
   // covers only the set it needs.
   // (a gathered batch waits for its row indices anyway: a shallow ring)
   constexpr int D = GATHER ? 2 : kWgDepth;
-  WgRegs<KB, QN> R[D];
-#pragma unroll
-  for (int s = 0; s < D; ++s) {
-    wg_load<KB, QN, GATHER>(P, Z, ldz, ncols, Q, ldq, rank, ccol, col_ok, seg_end, lc, R[s]);
+  std::conditional_t<Z8, WgRegs8<KB, QN>, WgRegs<KB, QN>> R[D];
+  auto load = [&](auto& Rs) {
+    if constexpr (Z8)
+      wg_load8<KB, QN, GATHER>(P, Q, ldq, rank, ccol, col_ok, chunk * (4 * 16 * QN), seg_end, lc, Rs);
+    else
+      wg_load<KB, QN, GATHER>(P, Z, ldz, ncols, Q, ldq, rank, ccol, col_ok, seg_end, lc, Rs);
     wg_advance(P, seg_end, lc);
-  }
+  };
+#pragma unroll
+  for (int s = 0; s < D; ++s) load(R[s]);
   for (int i = 0; i < nsteps; i += D) {
 #pragma unroll
     for (int s = 0; s < D; ++s) {
-      wg_commit_q<KB, QN>(R[s], Qt[s]);
+      wg_commit_q<KB>(R[s], Qt[s]);
+      if constexpr (Z8) {
+        if (threadIdx.x < QN * 16) Es[s][threadIdx.x >> 5][threadIdx.x & 31] = q8_scale(R[s].e);
+      }
       __syncthreads();
-      wg_compute<KB, QN>(R[s], Qt[s], acc);
-      wg_load<KB, QN, GATHER>(P, Z, ldz, ncols, Q, ldq, rank, ccol, col_ok, seg_end, lc, R[s]);
-      wg_advance(P, seg_end, lc);
+      bf16x8 fa[QN];
+      if constexpr (Z8) {
+        // e4m3 times its power of two is exact in bf16
+        const float* es = &Es[s][QN == 4 ? wave >> 1 : 0][8 * g];
+        const f32x4 s0 = *reinterpret_cast<const f32x4*>(es), s1 = *reinterpret_cast<const f32x4*>(es + 4);
+        uint32_t zb[8][QN / 2];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float sc = e < 4 ? s0[e & 3] : s1[e & 3];
+          zb[e][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(R[s].z[e], sc, false));
+          if constexpr (QN == 4)
+            zb[e][QN / 2 - 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(R[s].z[e], sc, true));
+        }
+        wg_transpose<QN>(zb, fa);
+      } else {
+        wg_transpose<QN>(R[s].z, fa);
+      }
+      wg_compute<KB, QN, EXACT>(fa, Qt[s], acc);
+      load(R[s]);
     }
   }
   // lane holds C[m = 4g + i][n = cl] of block (q, kb): column c0 + QN*m + q
@@ -334,9 +430,12 @@ __device__ __forceinline__ void wgrad_item(const WgradPlan& P, int job, int kind
   }
 }
 
-template <bool GATHER>
+// X8: x is an 8-bit checkpoint. Its gradients are held to the error of fp32
+// sums (three-part Q): the second part alone would leave about 3e-6.
+template <bool GATHER, bool X8>
 __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradPlan P) {
   __shared__ alignas(16) float Qt[kWgDepth][128][kQtLd];
+  __shared__ alignas(16) float Es[X8 ? kWgDepth : 1][2][32];
   __shared__ int job_of_item;
   // locate the job with one parallel read of the item table (thread j checks
   // job j); items are laid out job by job, dB chunks before dA chunks
@@ -353,11 +452,16 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradPlan P) {
   const int local = item - P.job_item0[job];
   const int kind = local < nb_db ? 0 : 1;
   const int chunk = kind == 0 ? local : local - nb_db;
+  auto run = [&](auto kb) {
+    constexpr int KB = decltype(kb)::value;
+    if (X8 && kind == 1) wgrad_item<KB, wgrad_qn(KB), GATHER, X8, X8>(P, job, kind, chunk, Qt, Es);
+    else wgrad_item<KB, wgrad_qn(KB), GATHER, false, X8>(P, job, kind, chunk, Qt, Es);
+  };
   switch (wgrad_kb(P.job_rank[job])) {
-    case 1: wgrad_item<1, wgrad_qn(1), GATHER>(P, job, kind, chunk, Qt); break;
-    case 2: wgrad_item<2, wgrad_qn(2), GATHER>(P, job, kind, chunk, Qt); break;
-    case 4: wgrad_item<4, wgrad_qn(4), GATHER>(P, job, kind, chunk, Qt); break;
-    default: wgrad_item<8, wgrad_qn(8), GATHER>(P, job, kind, chunk, Qt); break;
+    case 1: run(std::integral_constant<int, 1>{}); break;
+    case 2: run(std::integral_constant<int, 2>{}); break;
+    case 4: run(std::integral_constant<int, 4>{}); break;
+    default: run(std::integral_constant<int, 8>{}); break;
   }
 }
 
@@ -399,10 +503,11 @@ int wgrad_items_for_rank(int rank, int h_in, int h_out) {
 }
 
 hipError_t launch_wgrad(const WgradPlan& P, int grid, hipStream_t stream) {
-  if (P.token_rows)
-    hipLaunchKernelGGL(wgrad_kernel<true>, dim3(grid), dim3(kThreads), 0, stream, P);
-  else
-    hipLaunchKernelGGL(wgrad_kernel<false>, dim3(grid), dim3(kThreads), 0, stream, P);
+  const dim3 g(grid), b(kThreads);
+  if (P.x8 && P.token_rows) hipLaunchKernelGGL((wgrad_kernel<true, true>), g, b, 0, stream, P);
+  else if (P.x8) hipLaunchKernelGGL((wgrad_kernel<false, true>), g, b, 0, stream, P);
+  else if (P.token_rows) hipLaunchKernelGGL((wgrad_kernel<true, false>), g, b, 0, stream, P);
+  else hipLaunchKernelGGL((wgrad_kernel<false, false>), g, b, 0, stream, P);
   return hipGetLastError();
 }
 

@@ -346,6 +346,13 @@ struct WgradPlan {
   int32_t seg_ntok[kMaxJobSeg];
   float* part_base;     // partial slots: slot s = dB part [h_out][r] then dA part [r][h_in]
   int64_t part_stride;  // floats per slot
+  // The dA operand as an 8-bit checkpoint (x above is then null): e4m3 rows,
+  // one exponent byte per row and 128 columns.
+  const uint8_t* x8;
+  int64_t ldx8;
+  const uint8_t* x8_exps;
+  int64_t ldx8_exps;
+  int32_t x8_rows;
 };
 
 // Sum of the token-range parts of split weight-gradient jobs: for adapter

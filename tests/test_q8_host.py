@@ -1,0 +1,227 @@
+"""8-bit operators without a GPU: the struct's layout, every refusal (all of
+them before any HIP call), calls without rows, and the 64-bit forms that the
+GPU tests compare with."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import lora_adapter_batching_amd as L
+from lora_adapter_batching_amd import binding as B
+from tests import q8_ref as R
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = 1 << 40  # an aligned stand-in address, never read
+
+
+def q8(rows=4, width=256, ld=256, lde=4, block_rows=1, values=P, exps=P):
+    return B.CQ8(values, ld, exps, lde, rows, width, block_rows)
+
+
+def status(fn, *args):
+    st = fn(*args)
+    return st, L.load().lora_last_error().decode()
+
+
+def test_struct_matches_the_c_header(tmp_path):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    names = [f for f, _ in B.CQ8._fields_]
+    src = '#include <stddef.h>\n#include <stdio.h>\n#include "lora_sgmv.h"\nint main(void) {\n'
+    src += '  printf("%zu\\n", sizeof(lora_q8_t));\n'
+    src += "".join(f'  printf("%zu\\n", offsetof(lora_q8_t, {n}));\n' for n in names) + "  return 0;\n}\n"
+    (tmp_path / "q.c").write_text(src)
+    exe = tmp_path / "q"
+    subprocess.run([cc, "-std=c99", "-I", os.path.join(ROOT, "include"), str(tmp_path / "q.c"), "-o", str(exe)], check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [ctypes.sizeof(B.CQ8)] + [getattr(B.CQ8, n).offset for n in names]
+
+
+BAD_Q8 = [
+    (dict(rows=-1), "rows"), (dict(width=0), "width"), (dict(width=12), "width"), (dict(ld=255), "row stride"),
+    (dict(ld=264), "row stride"), (dict(width=264, ld=272), "row stride"), (dict(lde=3), "exponent stride"),
+    (dict(width=1024, ld=1024, lde=4), "exponent stride"), (dict(block_rows=2), "block_rows"),
+    (dict(values=0), "NULL"), (dict(exps=0), "NULL"), (dict(values=P + 8), "aligned"), (dict(exps=P + 2), "aligned"),
+]
+
+
+@pytest.mark.parametrize("bad,word", BAD_Q8)
+def test_every_entry_refuses_a_bad_store(bad, word):
+    lib = L.load()
+    b = q8(**bad)
+    r = ctypes.byref(b)
+    w = ctypes.byref(q8(rows=8, block_rows=128))
+    wbad = ctypes.byref(q8(**{"rows": 8, "block_rows": 128, **bad}))
+    calls = [(lib.lora_q8_quantize, P, 1024, r, None, None), (lib.lora_q8_dequantize, r, P, 1024, None),
+             (lib.lora_q8_matmul, r, w, P, 1024, 0, None), (lib.lora_q8_matmul, ctypes.byref(q8()), wbad, P, 1024, 0, None),
+             (lib.lora_swiglu, P, 2048, max(b.rows, 0), 256, None, 0, r, None),
+             (lib.lora_swiglu_backward, P, 2048, P, 1024, max(b.rows, 0), 128, None, 0, r, None)]
+    for fn, *args in calls:
+        st, msg = status(fn, *args)
+        assert st == B.LORA_INVALID_ARGUMENT, (fn, msg)
+        assert word in msg, msg
+
+
+def test_quantize_refusals():
+    lib = L.load()
+    o = q8()
+    for args, word in [((0, 256, o, None), "NULL"), ((P + 4, 256, o, None), "aligned"), ((P, 248, o, None), "below its width"),
+                       ((P, 260, o, None), "multiple of 8"), ((P, 256, None, None), "NULL"),
+                       ((P, 256, o, q8(rows=256, width=8, ld=128, block_rows=128)), "128 x 128"),
+                       ((P, 256, q8(rows=8, block_rows=128), q8(rows=248, width=8, ld=128, block_rows=128)), "transpose"),
+                       ((P, 256, q8(rows=8, block_rows=128), q8(rows=256, width=8, ld=128)), "block_rows")]:
+        st, msg = status(lib.lora_q8_quantize, args[0], args[1], ctypes.byref(args[2]) if args[2] else None,
+                         ctypes.byref(args[3]) if args[3] else None, None)
+        assert st == B.LORA_INVALID_ARGUMENT and word in msg, (args, msg)
+    for x, ld, word in [(0, 256, "NULL"), (P + 2, 256, "aligned"), (P, 128, "below its width")]:
+        st, msg = status(lib.lora_q8_dequantize, ctypes.byref(o), x, ld, None)
+        assert st == B.LORA_INVALID_ARGUMENT and word in msg, msg
+
+
+def test_matmul_refusals():
+    lib = L.load()
+    x, w = q8(), q8(rows=16, block_rows=128)
+    by, D = ctypes.byref, 1 << 41
+    for args, word, want in [
+            ((None, by(w), P, 16, 0), "NULL", 1), ((by(x), None, P, 16, 0), "NULL", 1),
+            ((by(x), by(q8(rows=16)), P, 16, 0), "block_rows", 1), ((by(w), by(w), P, 16, 0), "block_rows", 1),
+            ((by(x), by(q8(rows=16, width=128, block_rows=128)), P, 16, 0), "wide", 1),
+            ((by(x), by(q8(rows=12, block_rows=128)), P, 16, 0), "multiple of 8", 1),
+            ((by(x), by(w), 0, 16, 0), "NULL", 1), ((by(x), by(w), P + 2, 16, 0), "aligned", 1),
+            ((by(x), by(w), P, 8, 0), "below its width", 1), ((by(x), by(w), P, 20, 0), "multiple of 8", 1),
+            ((by(x), by(w), P, 16, 2), "flags", 1),
+            ((by(q8(ld=1 << 24)), by(w), D, 16, 0), "strides", 2), ((by(x), by(q8(rows=16, ld=1 << 24, block_rows=128)), D, 16, 0), "strides", 2),
+            ((by(q8(lde=1 << 24)), by(w), D, 16, 0), "strides", 2),
+            ((by(x), by(w), P, 16, 0), "starts at an operand", 1)]:
+        st, msg = status(lib.lora_q8_matmul, *args, None)
+        assert st == want and word in msg, (msg, word)
+
+
+def test_swiglu_refusals():
+    lib = L.load()
+    hq, gq = q8(rows=4, width=128, ld=128), q8(rows=4, width=256)
+    by = ctypes.byref
+    D = 1 << 41
+    for args, word in [((P, 256, -1, 128, D, 128, None), "num_tokens"), ((P, 256, 4, 12, D, 128, None), "width"),
+                       ((P, 256, 4, 0, D, 128, None), "width"), ((P, 256, 4, 128, None, 0, None), "both NULL"),
+                       ((0, 256, 4, 128, D, 128, None), "NULL"), ((P + 2, 256, 4, 128, D, 128, None), "aligned"),
+                       ((P, 248, 4, 128, D, 128, None), "below its width"), ((P, 256, 4, 128, D, 120, None), "below its width"),
+                       ((P, 256, 5, 128, None, 0, by(hq)), "expected 5"), ((P, 256, 4, 136, None, 0, by(hq)), "expected 4"),
+                       ((P, 256, 4, 128, P, 256, None), "starts at")]:
+        st, msg = status(lib.lora_swiglu, *args, None)
+        assert st == B.LORA_INVALID_ARGUMENT and word in msg, (args, msg)
+    for args, word in [((P, 256, D, 128, -1, 128, D * 2, 256, None), "num_tokens"), ((P, 256, 0, 128, 4, 128, D * 2, 256, None), "NULL"),
+                       ((P, 256, D, 120, 4, 128, D * 2, 256, None), "below its width"), ((P, 256, D, 128, 4, 128, None, 0, None), "both NULL"),
+                       ((P, 256, D, 128, 4, 128, D * 2, 128, None), "below its width"),
+                       ((P, 256, D, 128, 4, 128, None, 0, by(hq)), "expected 4 x 256"), ((P, 256, D, 128, 5, 128, None, 0, by(gq)), "expected 5"),
+                       ((P, 256, D, 128, 4, 128, P, 256, None), "starts at"), ((P, 256, D, 128, 4, 128, D, 256, None), "starts at")]:
+        st, msg = status(lib.lora_swiglu_backward, *args, None)
+        assert st == B.LORA_INVALID_ARGUMENT and word in msg, (args, msg)
+
+
+def _backward_args(x=None, T=4, rows=None, u=P, **seg):
+    ranks, scales = np.array([4, 8], np.int32), np.ones(2, np.float32)
+    ad = B.CAdapters(2, 256, 128, P, P, ranks.ctypes.data, scales.ctypes.data, 0, 0)
+    starts, adap = np.array([0, T], np.int32), np.array([0], np.int32)
+    sg = B.CSegments(T, 1, starts.ctypes.data, adap.ctypes.data, seg.get("rows_dev", 0), 0)
+    xs = x if x is not None else q8(rows=T if rows is None else rows)
+    keep = (ranks, scales, starts, adap, ad, sg, xs)
+    return keep, (ctypes.byref(xs), P, 128, u, 8, ctypes.byref(ad), ctypes.byref(sg), P, 256, P, P)
+
+
+def test_backward_refusals():
+    lib = L.load()
+
+    def call(want, word, args, flags=0, ws=P, wb=1 << 40):
+        keep, a = args
+        st, msg = status(lib.lora_packed_backward_q8, *a, flags, ws, wb, None)
+        assert st == want and word in msg, msg
+
+    call(1, "u is NULL", _backward_args(u=0))
+    call(1, "x has 3 rows", _backward_args(rows=3))
+    call(1, "wide", _backward_args(x=q8(width=128)))
+    call(1, "block_rows", _backward_args(x=q8(block_rows=128)))
+    call(1, "values/exps", _backward_args(x=q8(values=0)))
+    call(2, "strides", _backward_args(x=q8(ld=1 << 26)))
+    call(1, "gather limit", _backward_args(x=q8(rows=200, ld=1 << 24), T=200, rows_dev=P))
+    call(1, "flags", _backward_args(), flags=2)
+    call(3, "workspace", _backward_args(), wb=16)
+    keep, a = _backward_args()
+    st, msg = status(lib.lora_packed_backward_q8, None, *a[1:], 0, P, 1 << 40, None)
+    assert st == 1 and "x is NULL" in msg
+
+
+def test_no_rows_is_no_work():
+    """No HIP call is made without rows: these succeed without a GPU."""
+    lib = L.load()
+    by = ctypes.byref
+    e = q8(rows=0, values=0, exps=0)
+    assert lib.lora_q8_quantize(None, 0, by(e), None, None) == 0
+    assert lib.lora_q8_dequantize(by(e), None, 0, None) == 0
+    assert lib.lora_q8_matmul(by(e), by(q8(rows=8, block_rows=128)), None, 0, 0, None) == 0
+    assert lib.lora_q8_matmul(by(q8()), by(q8(rows=0, block_rows=128)), None, 0, 0, None) == 0
+    assert lib.lora_swiglu(None, 0, 0, 256, P, 256, by(e), None) == 0
+    assert lib.lora_swiglu_backward(None, 0, None, 0, 0, 128, None, 0, by(e), None) == 0
+
+
+def test_binding_refuses_wrong_tensors():
+    v, e = torch.zeros((4, 256), dtype=torch.uint8), torch.zeros((4, 4), dtype=torch.uint8)
+    L.Q8Rows(v, e, 256), L.Q8Rows(v.view(torch.float8_e4m3fn), e, 136), L.Q8Rows(v, e, 256, rows=2)
+    for args in [(v.float(), e, 256), (v, e.int(), 256), (v, e, 264), (v.t(), e, 4), (v, e[:3], 256), (v, e[:, :1], 256),
+                 (v[0], e, 256)]:
+        with pytest.raises(ValueError):
+            L.Q8Rows(*args)
+    with pytest.raises(ValueError):
+        L.Q8Rows(v, e, 256, rows=5)
+    with pytest.raises(ValueError):  # a stride of two bytes holds two blocks, but not in whole dwords
+        L.Q8Rows(v, torch.zeros((4, 2), dtype=torch.uint8), 256)
+    q, w = L.new_q8_rows(4, 256, "cpu"), L.new_q8_weights(16, 256, "cpu")
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    for fn, args in [(L.q8_quantize, (bf(3, 256), q)), (L.q8_quantize, (bf(4, 128), q)), (L.q8_quantize, (torch.zeros(4, 256), q)),
+                     (L.q8_dequantize, (q, bf(4, 255))), (L.q8_matmul, (q, w, bf(4, 8))), (L.q8_matmul, (q, w, bf(3, 16))),
+                     (L.swiglu, (bf(4, 256), bf(4, 256))), (L.swiglu, (torch.zeros(4, 256), bf(4, 128))),
+                     (L.swiglu_backward, (bf(4, 256), bf(4, 120), bf(4, 256))), (L.swiglu_backward, (bf(4, 256), bf(4, 128), bf(4, 128)))]:
+        with pytest.raises(ValueError):
+            fn(*args)
+    with pytest.raises(ValueError, match="device tensors"):
+        L.q8_quantize(bf(4, 256), q)
+
+
+def test_reference_rounding_is_nearest_even_on_every_code():
+    """The 64-bit rounding against a search over the whole e4m3 table."""
+    grid = np.unique(R.TABLE[np.isfinite(R.TABLE) & (R.TABLE >= 0)])
+    assert grid[-1] == 448 and len(grid) == 127
+    mids = (grid[1:] + grid[:-1]) / 2
+    v = np.concatenate([grid, mids, np.nextafter(mids, 0), np.nextafter(mids, 1e9), [0.0]])
+    got = R.round_e4m3(v)
+    for x, q in zip(v, got):
+        d = np.abs(grid - x)
+        near = np.flatnonzero(d == d.min())
+        want = grid[near[0]] if len(near) == 1 else grid[[n for n in near if n % 2 == 0][0]]
+        assert q == want, x
+
+
+def test_reference_exponent_is_the_smallest_that_fits():
+    rng = np.random.default_rng(0)
+    x = np.ldexp(rng.uniform(0.5, 1, 500), rng.integers(-130, 128, 500))[:, None]
+    e = R.block_exponents(x, 1)[:, 0]
+    assert np.all(x[:, 0] <= np.ldexp(448.0, e - 127))
+    assert np.all((x[:, 0] > np.ldexp(448.0, e - 128)) | (e == 1))
+
+
+def test_reference_swiglu_gradient_against_differences():
+    rng = np.random.default_rng(1)
+    x, dh = rng.standard_normal((3, 32)) * 2, rng.standard_normal((3, 16))
+    g = R.swiglu_grad(x, dh)
+    step = 1e-6
+    for i in range(3):
+        for j in range(32):
+            d = np.zeros_like(x)
+            d[i, j] = step
+            num = (np.sum(dh * R.swiglu(x + d)[3]) - np.sum(dh * R.swiglu(x - d)[3])) / (2 * step)
+            assert abs(num - g[i, j]) < 1e-7 * (1 + abs(num)), (i, j)  # step^2 and 1e-16 / step
