@@ -104,7 +104,7 @@ def load(path: str = LIB_PATH):
                                               ctypes.POINTER(ctypes.c_size_t)]
     lib.lora_sgmv_fused_graph.argtypes = [P, I64, ctypes.POINTER(CGraphAdapters), P, ctypes.c_int32, P, I64,
                                           P, ctypes.c_size_t, P]
-    Q = ctypes.POINTER(CQ8)
+    Q = P  # address of a CQ8
     lib.lora_q8_quantize.argtypes = [P, I64, Q, Q, P]
     lib.lora_q8_dequantize.argtypes = [Q, P, I64, P]
     lib.lora_q8_matmul.argtypes = [Q, Q, P, I64, ctypes.c_uint32, P]
@@ -412,16 +412,10 @@ class _Q8:
         if values.device != exps.device:
             raise ValueError(f"values are on {values.device}, exps on {exps.device}")
         self.values, self.exps = values, exps
+        self.dev = values.get_device()
         self._c = CQ8(_ptr(values), values.stride(0), _ptr(exps), exps.stride(0), self.rows, self.width,
                       self.block_rows)
-
-    @property
-    def c(self):
-        return ctypes.byref(self._c)
-
-    @property
-    def device(self):
-        return self.values.device
+        self.addr = ctypes.addressof(self._c)
 
 
 class Q8Rows(_Q8):
@@ -450,85 +444,101 @@ def new_q8_weights(rows: int, width: int, device="cuda") -> Q8Weights:
     return _new_q8(Q8Weights, rows, width, device)
 
 
-def _rows_arg(name: str, t, rows: int, width: int, device):
+def _rows_arg(name: str, t, rows: int, width: int, dev: int) -> int:
+    """The row stride of a bfloat16 [>= rows, width] tensor on GPU `dev`."""
     import torch
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.stride(1) != 1 or t.shape[0] < rows or t.shape[1] != width:
-        raise ValueError(f"{name} must be a bfloat16 [>= {rows}, {width}] matrix with unit column stride, "
-                         f"got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype is torch.bfloat16 and t.get_device() == dev:
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 2 and shape[0] >= rows and shape[1] == width and stride[1] == 1:
+            return stride[0]
+    raise ValueError(f"{name} must be a bfloat16 [>= {rows}, {width}] matrix with unit column stride on "
+                     f"{_dev_name(dev)}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _call_on(device, stream, fn, *args):
-    """Calls fn(*args, stream) with `device` current, on `stream` or the
-    device's current stream."""
+def _q8_arg(name: str, q: _Q8, dev: int) -> int:
+    if q.dev != dev:
+        raise ValueError(f"{name} is on {_dev_name(q.dev)}, expected {_dev_name(dev)}")
+    return q.addr
+
+
+def _dev_name(dev: int) -> str:
+    return f"cuda:{dev}" if dev >= 0 else "cpu"
+
+
+def _call_on(dev: int, stream, fn, *args):
+    """Calls fn(*args, stream) with GPU `dev` current, on `stream` or that
+    GPU's current stream. (A decode step makes many such calls and each is a
+    few microseconds of GPU work, so the host's share is kept small.)"""
     import torch
-    if device.type != "cuda":
-        raise ValueError(f"device tensors are needed, got {device}")
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _check(fn(*args, _stream_handle(stream)))
-    _check(fn(*args, _stream_handle(stream)))
+    if dev < 0:
+        raise ValueError("device tensors are needed, got cpu")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call_on(dev, stream, fn, *args)
+    st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream))
+    if st:
+        _check(st)
 
 
 def q8_quantize(x, out: _Q8, out_t: Optional[Q8Weights] = None, stream=None):
     """Stores bf16 x in 8 bits (Q8Rows or Q8Weights); with out_t the
     transposed weights too."""
-    _rows_arg("x", x, out.rows, out.width, out.device)
-    if out_t is not None and out_t.device != out.device:
-        raise ValueError(f"out_t is on {out_t.device}, expected {out.device}")
-    _call_on(out.device, stream, load().lora_q8_quantize, _ptr(x), x.stride(0), out.c,
-             out_t.c if out_t is not None else None)
+    dev = out.dev
+    ldx = _rows_arg("x", x, out.rows, out.width, dev)
+    ot = _q8_arg("out_t", out_t, dev) if out_t is not None else None
+    _call_on(dev, stream, (_lib or load()).lora_q8_quantize, x.data_ptr(), ldx, out.addr, ot)
 
 
 def q8_dequantize(q: _Q8, x, stream=None):
     """Restores an 8-bit matrix to bf16 x."""
-    _rows_arg("x", x, q.rows, q.width, q.device)
-    _call_on(q.device, stream, load().lora_q8_dequantize, q.c, _ptr(x), x.stride(0))
+    ldx = _rows_arg("x", x, q.rows, q.width, q.dev)
+    _call_on(q.dev, stream, (_lib or load()).lora_q8_dequantize, q.addr, x.data_ptr(), ldx)
 
 
 def q8_matmul(x: Q8Rows, w: Q8Weights, y, accumulate: bool = False, stream=None):
     """y = x w^T (or y += x w^T) on 8-bit operands; y bf16 [x.rows, w.rows]."""
-    _rows_arg("y", y, x.rows, w.rows, x.device)
-    if w.device != x.device:
-        raise ValueError(f"w is on {w.device}, expected {x.device}")
-    _call_on(x.device, stream, load().lora_q8_matmul, x.c, w.c, _ptr(y), y.stride(0), 1 if accumulate else 0)
+    dev = x.dev
+    ldy = _rows_arg("y", y, x.rows, w.rows, dev)
+    _call_on(dev, stream, (_lib or load()).lora_q8_matmul, x.addr, _q8_arg("w", w, dev), y.data_ptr(), ldy,
+             1 if accumulate else 0)
 
 
 def packed_backward_q8(x: Q8Rows, dy, u, adapters: Adapters, segments: Segments, dx, dA_ptrs, dB_ptrs,
                        flags: int = 0, ws=None, stream=None):
     """packed_backward with x as the 8-bit checkpoint; u (the forward's
     u_save) is required."""
+    T, dev = segments.num_tokens, x.dev
+    lddy = _rows_arg("dy", dy, T, adapters.h_out, dev)
+    lddx = _rows_arg("dx", dx, T, adapters.h_in, dev) if dx is not None else 0
+    if u is None or u.get_device() != dev or u.dim() != 2 or u.shape[0] < T or u.stride(1) != 1 or u.element_size() != 4:
+        raise ValueError(f"u must be a float32 [>= {T}, >= largest rank] matrix with unit column stride on {_dev_name(dev)}")
     wp, wb = _ws(ws)
-    _call_on(x.device, stream, load().lora_packed_backward_q8, x.c, _ptr(dy), dy.stride(0) if dy is not None else 0,
-             _ptr(u), u.stride(0) if u is not None else 0, adapters.c, segments.c, _ptr(dx),
-             dx.stride(0) if dx is not None else 0, _ptr(dA_ptrs), _ptr(dB_ptrs), int(flags), wp, wb)
+    _call_on(dev, stream, (_lib or load()).lora_packed_backward_q8, x.addr, dy.data_ptr(), lddy, u.data_ptr(),
+             u.stride(0), adapters.c, segments.c, _ptr(dx), lddx, _ptr(dA_ptrs), _ptr(dB_ptrs), int(flags), wp, wb)
 
 
 def swiglu(gate_up, h=None, hq: Optional[Q8Rows] = None, stream=None):
     """h = silu(gate) * up of gate_up [T, 2F], as bf16 rows and/or 8-bit rows."""
-    T, F = int(gate_up.shape[0]), int(gate_up.shape[1]) // 2
-    _rows_arg("gate_up", gate_up, T, 2 * F, gate_up.device)
-    if h is not None:
-        _rows_arg("h", h, T, F, gate_up.device)
-    if hq is not None and hq.device != gate_up.device:
-        raise ValueError(f"hq is on {hq.device}, expected {gate_up.device}")
-    _call_on(gate_up.device, stream, load().lora_swiglu, _ptr(gate_up), gate_up.stride(0), T, F, _ptr(h),
-             h.stride(0) if h is not None else 0, hq.c if hq is not None else None)
+    T, W = gate_up.shape
+    dev = gate_up.get_device()
+    F = W // 2
+    ld = _rows_arg("gate_up", gate_up, T, 2 * F, dev)
+    ldh = _rows_arg("h", h, T, F, dev) if h is not None else 0
+    q = _q8_arg("hq", hq, dev) if hq is not None else None
+    _call_on(dev, stream, (_lib or load()).lora_swiglu, gate_up.data_ptr(), ld, T, F, _ptr(h), ldh, q)
 
 
 def swiglu_backward(gate_up, dh, dgate_up=None, dgate_up_q: Optional[Q8Rows] = None, stream=None):
     """The gradient of swiglu's input, [T, 2F], as bf16 rows and/or 8-bit rows."""
-    T, F = int(gate_up.shape[0]), int(gate_up.shape[1]) // 2
-    _rows_arg("gate_up", gate_up, T, 2 * F, gate_up.device)
-    _rows_arg("dh", dh, T, F, gate_up.device)
-    if dgate_up is not None:
-        _rows_arg("dgate_up", dgate_up, T, 2 * F, gate_up.device)
-    if dgate_up_q is not None and dgate_up_q.device != gate_up.device:
-        raise ValueError(f"dgate_up_q is on {dgate_up_q.device}, expected {gate_up.device}")
-    _call_on(gate_up.device, stream, load().lora_swiglu_backward, _ptr(gate_up), gate_up.stride(0), _ptr(dh),
-             dh.stride(0), T, F, _ptr(dgate_up), dgate_up.stride(0) if dgate_up is not None else 0,
-             dgate_up_q.c if dgate_up_q is not None else None)
+    T, W = gate_up.shape
+    dev = gate_up.get_device()
+    F = W // 2
+    ld = _rows_arg("gate_up", gate_up, T, 2 * F, dev)
+    lddh = _rows_arg("dh", dh, T, F, dev)
+    ldd = _rows_arg("dgate_up", dgate_up, T, 2 * F, dev) if dgate_up is not None else 0
+    q = _q8_arg("dgate_up_q", dgate_up_q, dev) if dgate_up_q is not None else None
+    _call_on(dev, stream, (_lib or load()).lora_swiglu_backward, gate_up.data_ptr(), ld, dh.data_ptr(), lddh, T, F,
+             _ptr(dgate_up), ldd, q)
 
 
 class CPlanItem(ctypes.Structure):

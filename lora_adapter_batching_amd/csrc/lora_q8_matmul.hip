@@ -16,6 +16,8 @@
 // and an expansion of every fragment.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "lora_internal.h"
 #include "lora_q8.h"
 
@@ -56,20 +58,12 @@ __device__ __forceinline__ f32x4 mfma8_16(i32x8 a, i32x8 b, f32x4 c, int ea, int
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, ea, 0, eb);
 }
 
-// LDS-destination loads whose k position is a scalar offset. The descriptor
+// LDS-destination load whose k position is a scalar offset. The descriptor
 // ends with the last valid row; rows behind it have vector offsets past its
 // end (with or without the scalar offset counted) and write zeros.
 __device__ __forceinline__ void load_lds16_at(i32x4 rsrc, uint32_t lds_addr, uint32_t voff, uint32_t soff) {
   int m0_out;
   asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds"
-               : "={m0}"(m0_out)
-               : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
-               : "memory");
-  (void)m0_out;
-}
-__device__ __forceinline__ void load_lds4_at(i32x4 rsrc, uint32_t lds_addr, uint32_t voff, uint32_t soff) {
-  int m0_out;
-  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dword %2, %3, %4 offen lds"
                : "={m0}"(m0_out)
                : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
                : "memory");
@@ -95,39 +89,78 @@ __device__ __forceinline__ void tile_of(const MatArgs& a, int b, int grid, int& 
 }
 
 // ---------------------------------------------------------------------------
-// Tiled product: BT tokens x BN columns per workgroup of WT x WN waves, the
-// sum in steps of one 128-column block through an S-deep ring of LDS stages.
-// A stage holds the w rows, the x rows (128 bytes each) and one dword (four
-// blocks' exponents) per token and per 128 columns. The 16-byte piece c of row
-// r sits at position c ^ swizzle(r), which spreads the 32 rows of a fragment
-// over the LDS banks; the loads write LDS directly, so the permutation is
+// Tiled product: BT tokens x BN columns per workgroup, the sum in steps of one
+// 128-column block through a ring of S LDS stages. A stage holds the tile's w
+// rows and x rows, 128 bytes each; the 16-byte piece c of row r sits at position
+// c ^ swizzle(r), which spreads the rows of a fragment over the LDS banks (no
+// conflicts counted). The loads write LDS directly, so the permutation is
 // applied to the address each lane reads from.
+//
+// Small products cut the sum into KS parts: KS groups of waves with a ring each
+// walk their own blocks side by side and their sums are added in group order,
+// because one step's chain (barrier, LDS reads, matrix instructions) takes 0.3
+// us however small the tile.
+//
+// What bounds the 256 x 256 tile: the matrix unit takes 2048 clocks a step, the
+// CU's load path 1024 for its 64 KB (measured alone: 1370 with every CU
+// loading). So
+//  - the loads of step i + S are issued one by one between the matrix
+//    instructions (in one piece, behind the barrier, they hold the wave until
+//    the load path has taken the stage: 428 us instead of 413 for 8192 tokens
+//    4096 -> 14336),
+//  - rows are loaded in whole 128-byte lines: steps of 64 columns with twice
+//    the stages took 1.5 times as long to load (439 us),
+//  - the fragments of the next half step are read from LDS into a second set of
+//    registers under the matrix instructions of the current half,
+//  - the tile's exponents are fetched once, all loads in flight together (one
+//    row after the other: 407 us instead of 390).
+// Now 390 us, 2.47 PFLOP/s; the increment per step runs at 3.0, the rest is each
+// tile's start and end (11 us of 56).
 // ---------------------------------------------------------------------------
-template <int BT_, int BN_, int WT_, int WN_, int S_>
+template <int BT_, int BN_, int WT_, int WN_, int S_, int KS_ = 1>
 struct Tile {
-  static constexpr int BT = BT_, BN = BN_, WT = WT_, WN = WN_, S = S_;
-  static constexpr int waves = WT * WN;
+  static constexpr int BT = BT_, BN = BN_, WT = WT_, WN = WN_, S = S_, KS = KS_;
+  static constexpr int waves = WT * WN;                 // of one group; KS groups share the sum
   static constexpr int TT = BT / WT, TN = BN / WN;      // a wave's tokens and columns
   static constexpr int FT = TT / 32, FN = TN / 32;      // its fragments
-  static constexpr int xoff = BN * 128, eoff = xoff + BT * 128;
-  static constexpr int edw = (BT + 64 + 64 * waves - 1) / (64 * waves) * 64 * waves;  // exponent dwords, whole waves
-  static constexpr int stage = eoff + edw * 4;
-  static constexpr int loads = (BT + BN) / 8 / waves + edw / 64 / waves;  // per wave and stage
+  static constexpr int stage = (BN + BT) * 128;
+  static constexpr int loads = stage / 1024 / waves;    // 1 KB (8 rows) each, per wave and step
+  static constexpr int per = FT * FN >= FT + FN ? 1 : 2;  // fragments read per multiplication
+  // Blocks of w a wave's columns lie in: one, or (tile widths that do not divide
+  // into 128) each fragment's own.
+  static constexpr int EW = (BN % 128 == 0 && 128 % TN == 0) || 128 % BN == 0 ? 1 : FN;
+  static constexpr int erows = BT + (EW == 1 ? (BN + 127) / 128 : (BN + 254) / 128);  // exponent rows: tokens, w blocks
+  static constexpr int ring = S * stage;                // one group's stages
+  static constexpr int eoff = KS * ring;
+  static constexpr int egrp = erows * 17 * 4;           // one group's exponents
   static constexpr int eprow = TN * 4 + 16;             // epilogue row of one token (fp32, padded)
-  static constexpr int epi = waves * 32 * eprow;
-  static constexpr int lds = S * stage > epi ? S * stage : epi;
-  static_assert((BT + BN) % (8 * waves) == 0 && TT % 32 == 0 && TN % 32 == 0, "whole loads and fragments");
-  static_assert(lds <= 160 * 1024, "fits the LDS");
+  static constexpr int parts = (KS - 1) * BT * BN * 4;  // the other groups' sums
+  static constexpr int epi = parts + waves * 32 * eprow;
+  static constexpr int used = eoff + KS * egrp;
+  static constexpr int lds = used > epi ? used : epi;
+  static_assert(stage % (1024 * waves) == 0 && TT % 32 == 0 && TN % 32 == 0, "whole loads and fragments");
+  static_assert(FT + FN <= per * FT * FN, "every fragment of the next half is read");
+  static_assert(S >= 2 && lds <= 160 * 1024, "fits the LDS");
 };
 
-__device__ __forceinline__ int swizzle(int row) { return row & 7; }
+// Exponents in LDS: rows of 17 dwords (16 with four blocks each, one of
+// padding against bank conflicts), refilled every kExpBlocks blocks (the first
+// dword may begin up to three blocks earlier).
+constexpr int kExpBlocks = 60;
+
+__device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
 
 template <class C, bool ADD>
-__global__ __launch_bounds__(64 * C::waves) void q8_tile_kernel(MatArgs a) {
+__global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs a) {
   __shared__ alignas(1024) uint8_t smem[C::lds];
   const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)smem);
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int grp = C::KS > 1 ? wave0 / C::waves : 0, wave = wave0 - grp * C::waves;
+  const int tid = threadIdx.x - grp * 64 * C::waves;
+  // blocks [k0, k1) of the sum are this group's; all groups make `steps` steps
+  const int steps = C::KS > 1 ? (a.nkb + C::KS - 1) / C::KS : a.nkb;
+  const int k0 = grp * steps, k1 = min(a.nkb, k0 + steps);
   int tt, tn;
   tile_of(a, blockIdx.x, gridDim.x, tt, tn);
   const int t0 = tt * C::BT, n0 = tn * C::BN;
@@ -135,104 +168,202 @@ __global__ __launch_bounds__(64 * C::waves) void q8_tile_kernel(MatArgs a) {
   const int64_t kbytes = (int64_t)a.nkb * 128;
   const i32x4 wr = mk_rsrc_words(a.w + (int64_t)n0 * a.ldw, (int64_t)(vn - 1) * a.ldw + kbytes);
   const i32x4 xr = mk_rsrc_words(a.x + (int64_t)t0 * a.ldx, (int64_t)(vt - 1) * a.ldx + kbytes);
-  const i32x4 xer = mk_rsrc_words(a.xe + (int64_t)t0 * a.ldxe, (int64_t)(vt - 1) * a.ldxe + ((a.nkb + 3) & ~3));
-  const int eb0 = n0 >> 7, vb = ((n0 + vn - 1) >> 7) - eb0 + 1;
-  const i32x4 wer = mk_rsrc_words(a.we + (int64_t)eb0 * a.ldwe, (int64_t)(vb - 1) * a.ldwe + ((a.nkb + 3) & ~3));
 
-  constexpr int PW = (C::BN + C::BT) / 8 / C::waves;  // 1 KB pieces (8 rows) per wave
   // Piece p of the wave: rows 8 (p * waves + wave) .. + 7 of the stage (w rows, then x rows).
-  uint32_t voff[PW];
+  uint32_t voff[C::loads];
 #pragma unroll
-  for (int p = 0; p < PW; ++p) {
+  for (int p = 0; p < C::loads; ++p) {
     const int r = 8 * (p * C::waves + wave) + (lane >> 3);
     const int c = (lane & 7) ^ swizzle(r);
     const bool isx = 8 * (p * C::waves + wave) >= C::BN;
     voff[p] = (uint32_t)(isx ? (int64_t)(r - C::BN) * a.ldx : (int64_t)r * a.ldw) + 16u * c;
   }
-  constexpr int PE = C::edw / 64 / C::waves;
-  uint32_t eoffs[PE];
+  uint8_t* const ring = smem + grp * C::ring;
+  const uint32_t ring0 = lds0 + (uint32_t)(grp * C::ring);
+  // Load p of block kb; behind the group's last one the descriptors are empty and the
+  // loads write zeros, so that every step issues (and waits for) the same
+  // number without a branch between them.
+  auto load = [&](int kb, int slot, int p) {
+    const int piece = p * C::waves + wave;
+    i32x4 r = 8 * piece >= C::BN ? xr : wr;
+    r[2] = kb < k1 ? r[2] : 0;
+    load_lds16_at(r, ring0 + (uint32_t)(slot * C::stage + piece * 1024), voff[p], (uint32_t)kb * 128u);
+  };
+
+  uint32_t* const es = reinterpret_cast<uint32_t*>(smem + C::eoff + grp * C::egrp);
+  const int eb0 = n0 >> 7, vb = ((n0 + vn - 1) >> 7) - eb0 + 1;
+  // The dwords with blocks kb0 .. of the group: 16 lanes per row, all loads in
+  // flight before the first is stored.
+  constexpr int EP = (C::erows + 4 * C::waves - 1) / (4 * C::waves);
+  auto load_exps = [&](int kb0, uint32_t (&v)[EP]) {
+    const int b = (kb0 & ~3) + 4 * (tid & 15);
 #pragma unroll
-  for (int p = 0; p < PE; ++p) {
-    const int i = 64 * (p * C::waves + wave);  // first dword of the piece
-    const bool isx = i < C::BT;
-    const int r = isx ? i + lane : i + lane - C::BT;
-    eoffs[p] = (uint32_t)((int64_t)r * (isx ? a.ldxe : a.ldwe));
-  }
-  auto issue = [&](int kb) {
-    const uint32_t st = lds0 + (uint32_t)(kb % C::S) * C::stage;
-#pragma unroll
-    for (int p = 0; p < PW; ++p) {
-      const int piece = p * C::waves + wave;
-      const bool isx = 8 * piece >= C::BN;
-      i32x4 r = wr;
-      if (isx) r = xr;
-      load_lds16_at(r, st + piece * 1024, voff[p], (uint32_t)kb * 128u);
+    for (int p = 0; p < EP; ++p) {
+      const int r = (tid >> 4) + p * 4 * C::waves;
+      const bool isx = r < C::BT;
+      const bool ok = b < k1 && (isx ? r < vt : r - C::BT < vb);
+      const uint8_t* src = isx ? a.xe + (int64_t)(t0 + r) * a.ldxe : a.we + (int64_t)(eb0 + r - C::BT) * a.ldwe;
+      v[p] = ok ? *reinterpret_cast<const uint32_t*>(src + b) : 0u;
     }
+  };
+  auto store_exps = [&](const uint32_t (&v)[EP]) {
 #pragma unroll
-    for (int p = 0; p < PE; ++p) {
-      const int i = 64 * (p * C::waves + wave);
-      i32x4 r = wer;
-      if (i < C::BT) r = xer;
-      load_lds4_at(r, st + C::eoff + i * 4, eoffs[p], (uint32_t)(kb & ~3));
+    for (int p = 0; p < EP; ++p) {
+      const int r = (tid >> 4) + p * 4 * C::waves;
+      if (r < C::erows) es[r * 17 + (tid & 15)] = v[p];
     }
   };
 
   const int wt = wave / C::WN, wn = wave % C::WN;
   const int m = lane & 31, h = lane >> 5;
   const int wrow = wn * C::TN + m, xrow = wt * C::TT + m;
-  const int edw_w = C::BT + (((n0 + wn * C::TN) >> 7) - eb0);
+  const int ncol0 = n0 + wn * C::TN;
   f32x16 acc[C::FT][C::FN];
 #pragma unroll
   for (int i = 0; i < C::FT; ++i)
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) acc[i][j] = zero_acc16();
 
+  struct Exps {
+    int w[C::EW], x[C::FT];
+  };
+  // Lane (m, h) reads pieces 4s + 2h and 4s + 2h + 1 of row m for half s.
+  const int p0 = ((2 * h) ^ swizzle(m)) * 16, p1 = ((2 * h + 1) ^ swizzle(m)) * 16;
+  auto read_frag = [&](int slot, int s, int row) {
+    const uint8_t* p = ring + slot * C::stage + row * 128;
+    return frag(*reinterpret_cast<const u32x4*>(p + (p0 ^ (64 * s))), *reinterpret_cast<const u32x4*>(p + (p1 ^ (64 * s))));
+  };
+  // The dwords that hold a step's exponents (those in LDS begin with kb0's);
+  // shifted to the step's byte apart from the read, which takes its time.
+  auto read_exps = [&](int kb, int kb0, Exps& e) {
+    const int d = (kb >> 2) - (kb0 >> 2);
 #pragma unroll
-  for (int s = 0; s < C::S - 1; ++s)
-    if (s < a.nkb) issue(s);
-  for (int kb = 0; kb < a.nkb; ++kb) {
-    // stage kb has landed (the later ones may still be in flight), and every
-    // wave is done with the stage that the next loads overwrite
-    if (kb + C::S - 1 <= a.nkb) wait_vm<(C::S - 2) * C::loads>();
-    else wait_vm<0>();
+    for (int j = 0; j < C::EW; ++j) e.w[j] = (int)es[(C::BT + ((ncol0 + 32 * j) >> 7) - eb0) * 17 + d];
+#pragma unroll
+    for (int i = 0; i < C::FT; ++i) e.x[i] = (int)es[(xrow + 32 * i) * 17 + d];
+  };
+  // Behind the group's last block the exponent is 0 (2^-127), not the byte that
+  // happens to follow: 255 there would make the empty stage's zeros NaN.
+  auto shift_exps = [&](int kb, const Exps& e) {
+    Exps o;
+    const int sh = 8 * (kb & 3), width = kb < k1 ? 8 : 0;
+#pragma unroll
+    for (int j = 0; j < C::EW; ++j) o.w[j] = (int)__builtin_amdgcn_ubfe((uint32_t)e.w[j], sh, width);
+#pragma unroll
+    for (int i = 0; i < C::FT; ++i) o.x[i] = (int)__builtin_amdgcn_ubfe((uint32_t)e.x[i], sh, width);
+    return o;
+  };
+  i32x8 fw[2][C::FN], fx[2][C::FT];
+  // Half s of the group's step i: multiplies fragment set s and reads set s ^ 1 (the next
+  // half). Half 1 issues the loads of step i + S into the stage of step i,
+  // which every wave has read by then.
+  auto half = [&](auto sc, const Exps& e, int i, int kb0, Exps& raw) {
+    constexpr int s = decltype(sc)::value;
+    constexpr int M = C::FT * C::FN;
+    const int slot = (i + s) % C::S;
+#pragma unroll
+    for (int n = 0; n < M; ++n) {
+      const int t = n / C::FN, j = n % C::FN;
+      acc[t][j] = mfma8_32(fw[s][j], fx[s][t], acc[t][j], e.w[C::EW == 1 ? 0 : j], e.x[t]);
+#pragma unroll
+      for (int f = n * C::per; f < (n + 1) * C::per && f < C::FN + C::FT; ++f) {
+        if (f < C::FN) fw[s ^ 1][f] = read_frag(slot, s ^ 1, wrow + 32 * f);
+        else fx[s ^ 1][f - C::FN] = read_frag(slot, s ^ 1, C::BN + xrow + 32 * (f - C::FN));
+      }
+      if constexpr (s == 1) {
+        // (behind the last block this reads a row that nothing uses)
+        if (n == M / 2) read_exps(k0 + i + 1, kb0, raw);
+#pragma unroll
+        for (int p = n * C::loads / M; p < (n + 1) * C::loads / M; ++p) load(k0 + i + C::S, i % C::S, p);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  {
+    uint32_t ev[EP];
+    load_exps(k0, ev);
+#pragma unroll
+    for (int s = 0; s < C::S; ++s)
+#pragma unroll
+      for (int p = 0; p < C::loads; ++p) load(k0 + s, s, p);
+    store_exps(ev);
+  }
+  wait_vm<(C::S - 1) * C::loads>();
+  wait_lds();
+  __builtin_amdgcn_s_barrier();
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j) fw[0][j] = read_frag(0, 0, wrow + 32 * j);
+#pragma unroll
+  for (int i = 0; i < C::FT; ++i) fx[0][i] = read_frag(0, 0, C::BN + xrow + 32 * i);
+  for (int i0 = 0; i0 < steps; i0 += kExpBlocks) {
+    const int kb0 = k0 + i0;
+    if (i0) {
+      uint32_t ev[EP];
+      load_exps(kb0, ev);
+      store_exps(ev);
+      wait_lds();
+      __builtin_amdgcn_s_barrier();
+    }
+    Exps raw;
+    read_exps(kb0, kb0, raw);
+    Exps e = shift_exps(kb0, raw);
+    const int i1 = min(steps, i0 + kExpBlocks);
+    for (int i = i0; i < i1; ++i) {
+      half(std::integral_constant<int, 0>{}, e, i, kb0, raw);
+      // step i is in registers; step i + 1 has landed (the later ones may still
+      // be in flight); the barrier makes both true for every wave
+      wait_vm<(C::S - 2) * C::loads>();
+      wait_lds();
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      half(std::integral_constant<int, 1>{}, e, i, kb0, raw);
+      e = shift_exps(k0 + i + 1, raw);
+    }
+    // the exponents are refilled only when every wave has read its last ones
     wait_lds();
     __builtin_amdgcn_s_barrier();
-    if (kb + C::S - 1 < a.nkb) issue(kb + C::S - 1);
-    const uint8_t* st = smem + (kb % C::S) * C::stage;
-    const uint32_t* es = reinterpret_cast<const uint32_t*>(st + C::eoff);
-    const int sh = 8 * (kb & 3);
-    const int ew = (int)(es[edw_w] >> sh);
-    int ex[C::FT];
-#pragma unroll
-    for (int i = 0; i < C::FT; ++i) ex[i] = (int)(es[xrow + 32 * i] >> sh);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int c0 = ((4 * s + 2 * h) ^ swizzle(m)) * 16, c1 = ((4 * s + 2 * h + 1) ^ swizzle(m)) * 16;
-      i32x8 fw[C::FN], fx[C::FT];
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        const uint8_t* p = st + (wrow + 32 * j) * 128;
-        fw[j] = frag(*reinterpret_cast<const u32x4*>(p + c0), *reinterpret_cast<const u32x4*>(p + c1));
-      }
-#pragma unroll
-      for (int i = 0; i < C::FT; ++i) {
-        const uint8_t* p = st + C::xoff + (xrow + 32 * i) * 128;
-        fx[i] = frag(*reinterpret_cast<const u32x4*>(p + c0), *reinterpret_cast<const u32x4*>(p + c1));
-      }
+  }
+  // The last steps' empty loads write LDS too: they end, in every wave, before
+  // it is used for anything else.
+  wait_vm<0>();
+  wait_lds();
+  __builtin_amdgcn_s_barrier();
+  if constexpr (C::KS > 1) {
+    // the groups' sums, added in group order
+    f32x4* const part = reinterpret_cast<f32x4*>(smem);
+    auto place = [&](int g, int i, int j, int q) {
+      return ((((g - 1) * C::waves + wave) * C::FT + i) * C::FN + j) * 256 + q * 64 + lane;
+    };
+    if (grp) {
 #pragma unroll
       for (int i = 0; i < C::FT; ++i)
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) acc[i][j] = mfma8_32(fw[j], fx[i], acc[i][j], ew, ex[i]);
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            part[place(grp, i, j, q)] =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     }
+    __syncthreads();
+    if (grp) return;
+#pragma unroll
+    for (int g = 1; g < C::KS; ++g)
+#pragma unroll
+      for (int i = 0; i < C::FT; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 v = part[place(g, i, j, q)];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][j][4 * q + c] += v[c];
+          }
   }
   // Epilogue through LDS, so that a row's columns leave in whole lines:
   // 32 tokens at a time in fp32, 8 columns per lane back.
-  wait_lds();
-  __builtin_amdgcn_s_barrier();
-  uint8_t* ep = smem + wave * 32 * C::eprow;
+  uint8_t* ep = smem + C::parts + wave * 32 * C::eprow;
   constexpr int LPR = C::TN / 8;        // lanes per row
-  constexpr int RPP = 64 / LPR;         // rows per pass
-  const int ncol = n0 + wn * C::TN + 8 * (lane % LPR);
 #pragma unroll
   for (int i = 0; i < C::FT; ++i) {
 #pragma unroll
@@ -243,11 +374,12 @@ __global__ __launch_bounds__(64 * C::waves) void q8_tile_kernel(MatArgs a) {
         *reinterpret_cast<f32x4*>(ep + m * C::eprow + (32 * j + 8 * q + 4 * h) * 4) = v;
       }
 #pragma unroll
-    for (int p = 0; p < 32 / RPP; ++p) {
-      const int r = p * RPP + lane / LPR;
+    for (int p = 0; p < LPR / 2; ++p) {  // 32 LPR pieces of 8 columns
+      const int r = (64 * p + lane) / LPR, c = (64 * p + lane) % LPR;
       const int t = t0 + wt * C::TT + 32 * i + r;
-      const f32x4 v0 = *reinterpret_cast<const f32x4*>(ep + r * C::eprow + (lane % LPR) * 32);
-      const f32x4 v1 = *reinterpret_cast<const f32x4*>(ep + r * C::eprow + (lane % LPR) * 32 + 16);
+      const int ncol = ncol0 + 8 * c;
+      const f32x4 v0 = *reinterpret_cast<const f32x4*>(ep + r * C::eprow + c * 32);
+      const f32x4 v1 = *reinterpret_cast<const f32x4*>(ep + r * C::eprow + c * 32 + 16);
       if (t < a.T && ncol < a.N) {
         uint16_t* yp = a.y + (int64_t)t * a.ldy + ncol;
         float f[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
@@ -343,7 +475,7 @@ template <class C>
 void launch_tile(MatArgs a, bool add, hipStream_t s) {
   a.tiles_t = (a.T + C::BT - 1) / C::BT;
   a.tiles_n = (a.N + C::BN - 1) / C::BN;
-  const dim3 grid((unsigned)a.tiles_t * (unsigned)a.tiles_n), blk(64 * C::waves);
+  const dim3 grid((unsigned)a.tiles_t * (unsigned)a.tiles_n), blk(64 * C::waves * C::KS);
   if (add) hipLaunchKernelGGL((q8_tile_kernel<C, true>), grid, blk, 0, s, a);
   else hipLaunchKernelGGL((q8_tile_kernel<C, false>), grid, blk, 0, s, a);
 }
@@ -355,15 +487,50 @@ void launch_few(const MatArgs& a, bool add, hipStream_t s) {
   else hipLaunchKernelGGL((q8_few_kernel<TF, false>), grid, blk, 0, s, a);
 }
 
-using Tile256 = Tile<256, 256, 2, 4, 2>;
-using Tile128 = Tile<128, 128, 2, 2, 2>;
+// Tiles to choose from. A workgroup of a tile takes about fixed + step * (its
+// blocks of the sum) microseconds while `slots` of them run, so a product takes
+// that times the rounds its tiles need. Measured on 256 CUs (us; the sum is n
+// blocks long): the largest tile has the best rate and needs the most of
+// them, the small ones fill the GPU where there are few tokens.
+//   tokens, k, n            256x256  128x128  128x128*  128x160  128x96  128x64  32x64  32x32
+//   8191, 4096, 4096            120      138       160      159     181     220
+//   2048, 4096, 4096             45       35        40
+//   1024, 4096, 4096                      27        21       22      31      30
+//   256, 2560, 19456             35       23        27       18      24      30     68    122
+//   128, 2560, 19456                      20        15       16      13      21     35     65
+//   512, 2560, 2560                       18        14       15      12      11     22     33
+//   100, 9728, 2560                       51        32                       25     15     23
+//   37, 9728, 2560                        48        31                       24     15     12
+// (* with three stages, one workgroup per CU; the other holds two)
+struct TileChoice {
+  int bt, bn, ks, slots;
+  float fixed, step;
+  void (*launch)(MatArgs, bool, hipStream_t);
+};
+const TileChoice kTiles[] = {
+    {256, 256, 1, 256, 11.6f, 1.40f, launch_tile<Tile<256, 256, 2, 2, 2>>},
+    {128, 128, 1, 512, 2.8f, 1.00f, launch_tile<Tile<128, 128, 2, 2, 2>>},
+    {128, 128, 1, 256, 6.9f, 0.34f, launch_tile<Tile<128, 128, 2, 2, 3>>},
+    {128, 160, 1, 256, 8.5f, 0.37f, launch_tile<Tile<128, 160, 4, 1, 3>>},
+    {128, 96, 1, 256, 7.0f, 0.26f, launch_tile<Tile<128, 96, 4, 1, 3>>},
+    {128, 64, 1, 256, 5.4f, 0.26f, launch_tile<Tile<128, 64, 2, 2, 3>>},
+    {32, 64, 4, 256, 4.0f, 0.56f, launch_tile<Tile<32, 64, 1, 2, 3, 4>>},
+    {32, 32, 6, 256, 3.8f, 0.65f, launch_tile<Tile<32, 32, 1, 1, 3, 6>>},
+};
 
 void launch_matmul(const MatArgs& a, bool add, hipStream_t s) {
-  if (a.T <= 16) launch_few<1>(a, add, s);
-  else if (a.T <= 32) launch_few<2>(a, add, s);
-  else if (a.T <= 64) launch_few<4>(a, add, s);
-  else if ((int64_t)((a.T + 255) / 256) * ((a.N + 255) / 256) >= 256) launch_tile<Tile256>(a, add, s);
-  else launch_tile<Tile128>(a, add, s);
+  // One matrix fragment of tokens: the weights' bytes are all that counts (16
+  // tokens, 2560 -> 19456: 15 us against 18 with 32 x 64 tiles; 9728 -> 2560: 12
+  // against 12; one token 11 against 17 and 9 against 11).
+  if (a.T <= 16) return launch_few<1>(a, add, s);
+  const TileChoice* best = &kTiles[0];  // (its grid is checked by the caller)
+  double least = 0.;
+  for (const TileChoice& c : kTiles) {
+    const int64_t tiles = ((int64_t)a.T + c.bt - 1) / c.bt * (((int64_t)a.N + c.bn - 1) / c.bn);
+    const double t = (double)((tiles + c.slots - 1) / c.slots) * (c.fixed + (double)c.step * ((a.nkb + c.ks - 1) / c.ks));
+    if (&c == best || (t < least && tiles <= 0x7fffffff)) best = &c, least = t;
+  }
+  best->launch(a, add, s);
 }
 
 }  // namespace
@@ -388,6 +555,8 @@ extern "C" int lora_q8_matmul(const lora_q8_t* x, const lora_q8_t* w, void* y, i
   const int64_t most = 0x7fffff00 / 256;
   if (x->ld > most || w->ld > most || x->ld_exps > most || w->ld_exps > most)
     return set_error(LORA_UNSUPPORTED, "row strides above %lld bytes are not supported", (long long)most);
+  if (((int64_t)x->rows + 255) / 256 * (((int64_t)w->rows + 255) / 256) > 0x7fffffff || x->rows > 0x7fffff00 || w->rows > 0x7fffff00)
+    return set_error(LORA_UNSUPPORTED, "y of %d x %d is too large for one call", x->rows, w->rows);
   MatArgs a{};
   a.x = x->values; a.ldx = x->ld; a.xe = x->exps; a.ldxe = x->ld_exps;
   a.w = w->values; a.ldw = w->ld; a.we = w->exps; a.ldwe = w->ld_exps;

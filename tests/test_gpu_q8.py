@@ -59,11 +59,12 @@ def strided(t, extra=8, fill=7.0):
 
 
 def wide_q8(T, W, pad=16, fill=0xAB, weights=False):
-    """An 8-bit store with a row and exponent stride of its own, pre-filled."""
+    """An 8-bit store with a row and exponent stride of its own, pre-filled
+    (the exponents with 255, which scales by NaN wherever it is used)."""
     cls = L.Q8Weights if weights else L.Q8Rows
     v = torch.full((T + 1, R.padded(W) + pad), fill, dtype=torch.uint8, device="cuda")
     nb = R.padded(W) // 128
-    e = torch.full((-(-T // cls.block_rows) + 1, -(-nb // 4) * 4 + 4), fill, dtype=torch.uint8, device="cuda")
+    e = torch.full((-(-T // cls.block_rows) + 1, -(-nb // 4) * 4 + 4), 255, dtype=torch.uint8, device="cuda")
     return cls(v, e, W, rows=T)
 
 
@@ -76,7 +77,7 @@ def stored(x, weights=False):
 # ---------------------------------------------------------------------------
 # Rows and weights in 8 bits
 # ---------------------------------------------------------------------------
-def check_store(q, x64, tail=0xAB):
+def check_store(q, x64, tail=0xAB, etail=255):
     v, e = R.quantize(x64, q.block_rows)
     T, W = x64.shape
     P, nb, nr = R.padded(W), R.padded(W) // 128, -(-T // q.block_rows)
@@ -86,8 +87,8 @@ def check_store(q, x64, tail=0xAB):
     assert np.array_equal(got, v, equal_nan=True)
     assert np.array_equal(np.signbit(got[v == 0]), np.signbit(v[v == 0]))
     assert not b[:T, W:P].any()                                    # the pad of the last block
-    for rest in (b[T:], b[:T, P:], eb[nr:], eb[:nr, nb:]):         # not ours
-        assert rest.size == 0 or np.all(rest == tail)
+    for rest, fill in ((b[T:], tail), (b[:T, P:], tail), (eb[nr:], etail), (eb[:nr, nb:], etail)):  # not ours
+        assert rest.size == 0 or fill is None or np.all(rest == fill)
 
 
 @pytest.mark.parametrize("T,W", [(1, 8), (1, 128), (3, 136), (7, 1000), (64, 2560), (130, 256), (1000, 3584), (4100, 2568)])
@@ -172,29 +173,38 @@ def powers(q):
     return np.where(v == 0, 0.0, np.ldexp(s, np.maximum((b >> 3) & 15, 1).astype(int) - 7))
 
 
-def grouped(q, w):
-    """Sum over the groups of eight of 7 * 2^(E - 13)."""
-    a, b = torch.from_numpy(powers(q)).cuda(), torch.from_numpy(powers(w)).cuda()
-    total = torch.zeros((a.shape[0], b.shape[0]), dtype=torch.float64, device="cuda")
+def gpu64(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def grouped(q, w, cols):
+    """Sum over the groups of eight of 7 * 2^(E - 13), for the given columns of y."""
+    a, b = gpu64(powers(q)), gpu64(powers(w)[cols].T)
+    total = torch.zeros((a.shape[0], b.shape[1]), dtype=torch.float64, device="cuda")
     for k in range(0, a.shape[1], 8):
         top = torch.zeros_like(total)
         for i in range(k, k + 8):
-            top = torch.maximum(top, a[:, i, None] * b[None, :, i])
+            torch.maximum(top, a[:, i, None] * b[None, i], out=top)
         total += top
-    return 7 * 2.0 ** -13 * total.cpu().numpy()
+    return 7 * 2.0 ** -13 * total
 
 
-def matmul_tolerance(q, w, ref, y0=None):
-    a, b = R.read_store(q), R.read_store(w)
-    mag = np.abs(a) @ np.abs(b.T) + (0 if y0 is None else np.abs(y0))
-    err = grouped(q, w) + (R.padded(a.shape[1]) + 2) * F32 * mag
-    return BF * (np.abs(ref) + err) + err
+def matmul_reference(q, w, y0=None, cols=slice(None)):
+    """(y, tolerance) in 64 bits, on the GPU."""
+    a, b = gpu64(R.read_store(q)), gpu64(R.read_store(w)[cols].T)
+    ref, mag = torch.matmul(a, b), torch.matmul(a.abs(), b.abs())
+    if y0 is not None:
+        ref, mag = ref + y0[:, cols].double(), mag + y0[:, cols].double().abs()
+    err = grouped(q, w, cols) + (R.padded(a.shape[1]) + 2) * F32 * mag
+    return ref, BF * (ref.abs() + err) + err
 
 
-def check_matmul(q, w, y, y0=None):
-    ref = R.read_store(q) @ R.read_store(w).T + (0 if y0 is None else y0)
-    with np.errstate(invalid="ignore"):
-        held(to_f64(y), ref, matmul_tolerance(q, w, ref, y0), "y")
+def check_matmul(q, w, y, y0=None, cols=slice(None)):
+    ref, tol = matmul_reference(q, w, y0, cols)
+    got = y[:, cols].double()
+    assert torch.equal(torch.isfinite(got), torch.isfinite(ref))
+    bad = (got - ref).abs() > tol
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} outside, worst {float((got - ref).abs()[bad].max())}"
 
 
 SHAPES = [(1, 8, 8), (1, 2560, 2560), (2, 136, 24), (15, 264, 1000), (16, 128, 128), (17, 1000, 72), (32, 512, 136), (33, 2568, 264),
@@ -218,8 +228,38 @@ def test_matmul(T, K, N):
     y0 = rows(rng, T, N)
     y.copy_(y0)
     L.q8_matmul(q, w, y, accumulate=True)
-    check_matmul(q, w, y, to_f64(y0))
+    check_matmul(q, w, y, y0)
     assert torch.all(big[T] == 7) and torch.all(big[:, N:] == 7)
+
+
+# Sums longer than the 60 blocks whose exponents a workgroup (or one of its
+# groups) holds at a time, and the largest tile; some columns of each are compared.
+LONG = [(4100, 4096, 8200), (4100, 8328, 8200), (2049, 7944, 4104), (1000, 8200, 4096), (256, 8200, 19456), (128, 8200, 19456),
+        (512, 8200, 2560), (100, 31000, 2560), (40, 46592, 2560), (9, 9728, 136)]
+
+
+@pytest.mark.parametrize("T,K,N", LONG)
+def test_matmul_long_sums(T, K, N):
+    rng = np.random.default_rng(T + K)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T * K)
+    x = (torch.randn((T, K), generator=g, device="cuda") * torch.exp(torch.randn((T, 1), generator=g, device="cuda"))).to(torch.bfloat16)
+    w = torch.randn((N, K), generator=g, device="cuda").to(torch.bfloat16)
+    q, p = stored(x), stored(w, weights=True)
+    y = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    L.q8_matmul(q, p, y)
+    cols = np.unique(np.concatenate([[0, 31, 32, 127, 128, N - 1], rng.integers(0, N, 24)]))
+    cols = cols[cols < N]
+    check_matmul(q, p, y, cols=cols)
+    again = torch.full_like(y, float("nan"))
+    L.q8_matmul(q, p, again)
+    assert torch.equal(y, again)
+    # the other columns: each row's sum of y against the sum of the weights' columns, off by at most the roundings of all of them
+    total = torch.matmul(gpu64(R.read_store(q)), gpu64(R.read_store(p).sum(0)[:, None]))[:, 0]
+    lim = (BF + 2.0 ** -9) * y.double().abs().sum(1) + 7 * 2.0 ** -13 * N * float(torch.finfo(torch.float32).eps)
+    ref_cols, tol_cols = matmul_reference(q, p, cols=cols)
+    lim += N * tol_cols.amax(1)
+    assert torch.all((y.double().sum(1) - total).abs() <= lim)
 
 
 def test_matmul_exact_integers():
@@ -270,7 +310,7 @@ def test_matmul_gradient_is_the_transposed_store():
     L.q8_matmul(dy, pt, dx)
     check_matmul(dy, pt, dx)
     d, wf = R.read_store(dy), R.read_store(p)
-    tol = matmul_tolerance(dy, pt, d @ wf)
+    tol = matmul_reference(dy, pt)[1].cpu().numpy()
     for t, k in [(0, 0), (69, 263), (33, 128)]:
         e = np.zeros((T, K))
         e[t, k] = 0.5
@@ -508,7 +548,7 @@ def test_calls_on_two_streams():
             L.swiglu(y, h, stream=s)
     torch.cuda.synchronize()
     for x, w, q, y, h, s in jobs:
-        check_store(q, to_f64(x), tail=0)
+        check_store(q, to_f64(x), etail=None)
         check_matmul(q, w, y)
         g, _, _, ref = R.swiglu(to_f64(y))
         err = np.abs(ref) * (np.abs(g) + 8) * 2.0 ** -22 + 1e-30

@@ -101,3 +101,41 @@ def test_part_loads_are_whole_device_scope_vectors(fwd_asm):
         assert re.search(r"buffer_load_dwordx4 .*\bsc1\b", body), k.split(":")[0]
         assert not re.search(r"buffer_load_dword v\d+, .*\bsc1\b", body), k.split(":")[0]
     assert n > 0
+
+
+@pytest.fixture(scope="module")
+def q8_matmul_asm(tmp_path_factory):
+    return _device_asm(os.path.join(CSRC, "lora_q8_matmul.hip"), tmp_path_factory.mktemp("asm"))
+
+
+def test_q8_matmul_lds_loads_scalar_operands_and_no_scratch(q8_matmul_asm):
+    """The 8-bit product's LDS-destination loads: M0, the descriptor and the k
+    offset are scalar registers, M0 has no other use, no kernel spills vectors
+    to memory, and the steps of the main loops hold no other vector memory
+    access (their explicit waits count the ring's loads)."""
+    in_asm, loads = False, 0
+    for l in q8_matmul_asm.splitlines():
+        if "ASMSTART" in l or "ASMEND" in l:
+            in_asm = "ASMSTART" in l
+            continue
+        s = l.split(";")[0].strip()
+        if in_asm:
+            m = re.match(r"s_mov_b32 m0, (\S+)", s)
+            if m:
+                assert re.fullmatch(r"s\d+|vcc_(lo|hi)", m.group(1)), s
+            if s.startswith("buffer_load"):
+                loads += 1
+                assert re.fullmatch(r"buffer_load_dwordx4 v\d+, s\[\d+:\d+\], (s\d+|vcc_(lo|hi)) offen lds", s), s
+        else:
+            assert not re.search(r"\bm0\b", s), s
+    assert loads > 0
+    sizes = re.findall(r"\.private_segment_fixed_size:\s+(\d+)", q8_matmul_asm)
+    assert sizes and all(int(v) == 0 for v in sizes), sizes
+    # between two barriers of the main loops nothing but the ring's loads
+    for k in re.split(r"\n(?=_ZN4lora\S*q8_tile_kernel\S*:)", q8_matmul_asm)[1:]:
+        body = k.split(".Lfunc_end")[0]
+        loops = [b for b in body.split("s_barrier") if b.count("v_mfma") and "buffer_load_dwordx4" in b]
+        assert loops
+        for b in loops:
+            inner = re.split(r"v_mfma", b)[1:-1]
+            assert not any(re.search(r"global_(load|store)|buffer_store|flat_", p) for p in inner), k.split(":")[0]
