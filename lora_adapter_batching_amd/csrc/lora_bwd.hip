@@ -123,17 +123,30 @@ struct WgRegs {
   float q[2 * KB];        // this thread's share of the step's Q tile
 };
 
-// An 8-bit Z (dA from a checkpoint): the same rows and columns as e4m3
-// bytes, and one exponent byte per token and 128 columns. An item's columns
-// (256 for QN = 4, 128 for QN = 2) are whole blocks and a wave's lie in one of
-// them, so thread i < 32 * blocks loads the byte of block i / 32, token i % 32,
-// and the step's scales go through LDS beside its Q tile.
-template <int KB, int QN>
-struct WgRegs8 {
-  uint32_t z[8];    // QN bytes each
-  uint32_t e;       // this thread's exponent byte
-  float q[2 * KB];
+// Gradients of a batch whose x is an 8-bit checkpoint. They are held to the
+// error of fp32 sums: Q enters as three bf16 parts (24 mantissa bits; two would
+// leave about 3e-6). The parts are made once per step, by the thread that loads
+// a pair of tokens' values, and go through LDS as MFMA operands; made in every
+// wave from fp32 in LDS, they took more time than the step's loads (dA and dB
+// of 65536 tokens, 3584 -> 3584, 32 adapters: 206 us).
+//
+// Z of dA is then e4m3: the same rows and columns as bytes, and one exponent
+// byte per token and 128 columns. An item's columns (256 for QN = 4, 128 for
+// QN = 2) are whole blocks and a wave's lie in one of them, so thread i < 32 *
+// blocks loads the byte of block i / 32, token i % 32, and the step's scales go
+// through LDS beside its Q tile.
+template <int KB, int QN, bool Z8>
+struct WgRegsX {
+  uint32_t z[8][Z8 ? 1 : QN / 2];  // Z rows 8g + e: QN bytes, or QN / 2 bf16 pairs
+  uint32_t e;                      // this thread's exponent byte (Z8)
+  float q[KB][2];                  // this thread's pairs of tokens of the step's Q tile
 };
+constexpr int kQxLd = 20;  // LDS row (dwords) of a part: 16 token pairs and padding against bank conflicts
+struct WgShareX {
+  uint32_t q[2][3][128][kQxLd];  // [buffer][part][rank][token pair]
+  float e[2][2][32];             // [buffer][block][token]
+};
+
 
 __device__ __forceinline__ void wg_advance(const WgradPlan& P, int seg_end, WgCursor& c) {
   c.t0 += 32;
@@ -198,57 +211,139 @@ __device__ __forceinline__ void wg_load(const WgradPlan& P, const uint16_t* Z, i
   }
 }
 
-// wg_load for an 8-bit Z. A row outside the checkpoint reads as zero.
-template <int KB, int QN, bool GATHER>
-__device__ __forceinline__ void wg_load8(const WgradPlan& P, const float* Q, int64_t ldq, int rank, int ccol,
-                                         bool col_ok, int col0, int seg_end, const WgCursor& c,
-                                         WgRegs8<KB, QN>& R) {
+// Loads of one step on the exact path. A row outside the matrix reads as zero.
+template <int KB, int QN, bool GATHER, bool Z8>
+__device__ __forceinline__ void wg_load_x(const WgradPlan& P, const uint16_t* Z, int64_t ldz, int ncols,
+                                          const float* Q, int64_t ldq, int rank, int ccol, bool col_ok, int col0,
+                                          int seg_end, const WgCursor& c, WgRegsX<KB, QN, Z8>& R) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const bool live = c.seg < seg_end;
   const int cnt = live ? min(32, c.tend - c.t0) : 0;
-  const int blocks = (P.h_in + kQ8Block - 1) / kQ8Block;
-  const int eb = (col0 >> 7) + (int)(threadIdx.x >> 5), et = threadIdx.x & 31;
-  const bool e_ok = (int)threadIdx.x < QN * 16 && eb < blocks && et < cnt;
-  __amdgpu_buffer_rsrc_t zr, er, rr;
-  if constexpr (GATHER) {
-    zr = mk_rsrc(P.x8, cnt > 0 ? kGatherSpan : 0);
-    er = mk_rsrc(P.x8_exps, cnt > 0 ? kGatherSpan : 0);
-    rr = mk_rsrc(P.token_rows + (live ? c.t0 : 0), (int64_t)cnt * 4);
-  } else {
-    const int64_t t0 = live ? c.t0 : 0;
-    zr = mk_rsrc(P.x8 + t0 * P.ldx8, cnt > 0 ? (int64_t)(cnt - 1) * P.ldx8 + P.h_in : 0);
-    er = mk_rsrc(P.x8_exps + t0 * P.ldx8_exps, cnt > 0 ? (int64_t)(cnt - 1) * P.ldx8_exps + blocks : 0);
-  }
-  // byte offset of column `col` of the step's row r in a matrix of stride ld
-  auto place = [&](int r, int64_t ld, int col, int bytes, bool ok) -> uint32_t {
+  const int64_t t0 = live ? c.t0 : 0;
+  __amdgpu_buffer_rsrc_t rr;
+  if constexpr (GATHER) rr = mk_rsrc(P.token_rows + t0, (int64_t)cnt * 4);
+  // byte offset of byte `at` of the step's row r in a matrix whose rows are
+  // `bytes` long and `ld` bytes apart
+  auto place = [&](int r, int64_t ld, int64_t at, int64_t bytes, int rows, bool ok) -> uint32_t {
     int64_t row_bytes = (int64_t)r * ld;
     if constexpr (GATHER) {
       const int32_t row = (int32_t)__builtin_amdgcn_raw_buffer_load_b32(rr, ok ? 4 * r : (int)kOff, 0, 0);
       row_bytes = (int64_t)row * ld;
-      ok = ok && row >= 0 && row < P.x8_rows && row_bytes <= kGatherSpan - bytes;
+      ok = ok && row >= 0 && row < rows && row_bytes <= kGatherSpan - bytes;
     }
-    return ok ? (uint32_t)(row_bytes + col) : kOff;
+    return ok ? (uint32_t)(row_bytes + at) : kOff;
   };
+  auto matrix = [&](const void* base, int64_t ld, int64_t bytes) {
+    if constexpr (GATHER) return mk_rsrc(base, cnt > 0 ? kGatherSpan : 0);
+    else return mk_rsrc(static_cast<const uint8_t*>(base) + t0 * ld, cnt > 0 ? (int64_t)(cnt - 1) * ld + bytes : 0);
+  };
+  if constexpr (Z8) {
+    const int blocks = (P.h_in + kQ8Block - 1) / kQ8Block;
+    const __amdgpu_buffer_rsrc_t zr = matrix(P.x8, P.ldx8, P.h_in), er = matrix(P.x8_exps, P.ldx8_exps, blocks);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int r = 8 * g + e;
-    const uint32_t off = place(r, P.ldx8, ccol, P.h_in, col_ok && r < cnt);
-    if constexpr (QN == 4) R.z[e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(zr, (int)off, 0, kNT);
-    else R.z[e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(zr, (int)off, 0, kNT);
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t off = place(8 * g + e, P.ldx8, ccol, P.h_in, P.x8_rows, col_ok && 8 * g + e < cnt);
+      if constexpr (QN == 4) R.z[e][0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(zr, (int)off, 0, kNT);
+      else R.z[e][0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(zr, (int)off, 0, kNT);
+    }
+    const int eb = (col0 >> 7) + (int)(threadIdx.x >> 5), et = threadIdx.x & 31;
+    const bool e_ok = (int)threadIdx.x < QN * 16 && eb < blocks && et < cnt;
+    R.e = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(er, (int)place(et, P.ldx8_exps, eb, blocks, P.x8_rows, e_ok), 0, 0);
+  } else {
+    const __amdgpu_buffer_rsrc_t zr = matrix(Z, ldz * 2, (int64_t)ncols * 2);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t off = place(8 * g + e, ldz * 2, (int64_t)ccol * 2, (int64_t)ncols * 2, 0x7fffffff, col_ok && 8 * g + e < cnt);
+      if constexpr (QN == 4) {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(zr, (int)off, 0, kNT);
+        R.z[e][0] = v[0];
+        R.z[e][QN / 2 - 1] = v[1];
+      } else {
+        R.z[e][0] = __builtin_amdgcn_raw_buffer_load_b32(zr, (int)off, 0, kNT);
+      }
+    }
   }
-  R.e = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(er, (int)place(et, P.ldx8_exps, eb, blocks, e_ok), 0, 0);
-  const __amdgpu_buffer_rsrc_t qr = mk_rsrc(Q + (int64_t)(live ? c.t0 : 0) * ldq, (int64_t)cnt * ldq * 4);
+  // Q (fp32, sorted positions): pair p holds tokens 2 tp, 2 tp + 1 of rank k
+  const __amdgpu_buffer_rsrc_t qr = mk_rsrc(Q + t0 * ldq, (int64_t)cnt * ldq * 4);
 #pragma unroll
-  for (int j = 0; j < 2 * KB; ++j) {
-    const int e2 = threadIdx.x + kThreads * j;
-    const int tt = e2 / (16 * KB), k = e2 - tt * (16 * KB);
-    const uint32_t off = (tt < cnt && k < rank) ? (uint32_t)(((int64_t)tt * ldq + k) * 4) : kOff;
-    R.q[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(qr, (int)off, 0, 0));
+  for (int p = 0; p < KB; ++p) {
+    const int e2 = threadIdx.x + kThreads * p;
+    const int tp = e2 / (16 * KB), k = e2 - tp * (16 * KB);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int tt = 2 * tp + h;
+      const uint32_t off = (tt < cnt && k < rank) ? (uint32_t)(((int64_t)tt * ldq + k) * 4) : kOff;
+      R.q[p][h] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(qr, (int)off, 0, 0));
+    }
   }
 }
 
-template <int KB, class Regs>
-__device__ __forceinline__ void wg_commit_q(const Regs& R, float (*Qt)[kQtLd]) {
+// The step's Q as three bf16 parts, and its scales, into buffer b.
+template <int KB, int QN, bool Z8>
+__device__ __forceinline__ void wg_commit_x(const WgRegsX<KB, QN, Z8>& R, WgShareX& sh, int b) {
+#pragma unroll
+  for (int p = 0; p < KB; ++p) {
+    const int e2 = threadIdx.x + kThreads * p;
+    const int tp = e2 / (16 * KB), k = e2 - tp * (16 * KB);
+    f32x2_t f = {R.q[p][0], R.q[p][1]};
+#pragma unroll
+    for (int part = 0; part < 3; ++part) {
+      const uint32_t v = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2_t));
+      sh.q[b][part][k][tp] = v;
+      f[0] -= __builtin_bit_cast(float, v << 16);
+      f[1] -= __builtin_bit_cast(float, v & 0xffff0000u);
+    }
+  }
+  if constexpr (Z8)
+    if (threadIdx.x < QN * 16) sh.e[b][threadIdx.x >> 5][threadIdx.x & 31] = q8_scale(R.e);
+}
+
+// acc += Z^T Q of the step in buffer b.
+template <int KB, int QN, bool Z8>
+__device__ __forceinline__ void wg_compute_x(const WgRegsX<KB, QN, Z8>& R, const WgShareX& sh, int b,
+                                             f32x4 (&acc)[QN][KB]) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, cl = lane & 15;
+  uint32_t z[8][QN / 2];
+  if constexpr (Z8) {
+    // e4m3 times its power of two is exact in bf16
+    const float* es = &sh.e[b][QN == 4 ? threadIdx.x >> 7 : 0][8 * g];
+    const f32x4 s0 = *reinterpret_cast<const f32x4*>(es), s1 = *reinterpret_cast<const f32x4*>(es + 4);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float sc = e < 4 ? s0[e & 3] : s1[e & 3];
+      z[e][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(R.z[e][0], sc, false));
+      if constexpr (QN == 4)
+        z[e][QN / 2 - 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(R.z[e][0], sc, true));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int q = 0; q < QN / 2; ++q) z[e][q] = R.z[e][q];
+  }
+  // A operand: frag q = Z[8g + e][column q], e = 0..7 (byte permutes of row pairs)
+  bf16x8 fa[QN];
+#pragma unroll
+  for (int q = 0; q < QN; ++q) {
+    u32x4 v;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      v[d] = __builtin_amdgcn_perm(z[2 * d + 1][q >> 1], z[2 * d][q >> 1], (q & 1) ? 0x07060302u : 0x05040100u);
+    fa[q] = as_bf16x8(v);
+  }
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int part = 0; part < 3; ++part) {
+      const bf16x8 fq = as_bf16x8(*reinterpret_cast<const u32x4*>(&sh.q[b][part][16 * kb + cl][4 * g]));
+#pragma unroll
+      for (int q = 0; q < QN; ++q) acc[q][kb] = mfma16(fa[q], fq, acc[q][kb]);
+    }
+}
+
+template <int KB, int QN>
+__device__ __forceinline__ void wg_commit_q(const WgRegs<KB, QN>& R, float (*Qt)[kQtLd]) {
 #pragma unroll
   for (int j = 0; j < 2 * KB; ++j) {
     const int e2 = threadIdx.x + kThreads * j;
@@ -257,27 +352,21 @@ __device__ __forceinline__ void wg_commit_q(const Regs& R, float (*Qt)[kQtLd]) {
   }
 }
 
-// A operand: frag q = Z[8g + e][column q], e = 0..7, from Z as bf16 pairs of
-// columns (register transpose)
-template <int QN>
-__device__ __forceinline__ void wg_transpose(const uint32_t (&z)[8][QN / 2], bf16x8 (&fa)[QN]) {
+template <int KB, int QN>
+__device__ __forceinline__ void wg_compute(const WgRegs<KB, QN>& R, float (*Qt)[kQtLd], f32x4 (&acc)[QN][KB]) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, cl = lane & 15;
+  // A operand: frag q = Z[8g + e][column q], e = 0..7 (register transpose)
+  bf16x8 fa[QN];
 #pragma unroll
   for (int q = 0; q < QN; ++q) {
     u32x4 v;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      const uint32_t lo = z[2 * d][q >> 1], hi = z[2 * d + 1][q >> 1];
+      const uint32_t lo = R.z[2 * d][q >> 1], hi = R.z[2 * d + 1][q >> 1];
       v[d] = (q & 1) ? ((lo >> 16) | (hi & 0xffff0000u)) : ((lo & 0xffffu) | (hi << 16));
     }
     fa[q] = as_bf16x8(v);
   }
-}
-
-// acc += Z^T Q of one step. EXACT: the fp32 Q enters as three bf16 parts
-// (24 mantissa bits) instead of two (16).
-template <int KB, int QN, bool EXACT>
-__device__ __forceinline__ void wg_compute(const bf16x8 (&fa)[QN], float (*Qt)[kQtLd], f32x4 (&acc)[QN][KB]) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, cl = lane & 15;
   // B operand: Q[8g + e][16kb + cl] as bf16 hi + lo
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
@@ -289,22 +378,20 @@ __device__ __forceinline__ void wg_compute(const bf16x8 (&fa)[QN], float (*Qt)[k
       f[e] = q0[e];
       f[4 + e] = q1[e];
     }
-    bf16x8 qh, ql, qx;
-    if constexpr (EXACT) split8(f, qh, ql, qx);
-    else split8(f, qh, ql);
+    bf16x8 qh, ql;
+    split8(f, qh, ql);
 #pragma unroll
     for (int q = 0; q < QN; ++q) {
       acc[q][kb] = mfma16(fa[q], qh, acc[q][kb]);
       acc[q][kb] = mfma16(fa[q], ql, acc[q][kb]);
-      if constexpr (EXACT) acc[q][kb] = mfma16(fa[q], qx, acc[q][kb]);
     }
   }
 }
 
-// Z8: Z is the 8-bit checkpoint (dA only). EXACT: see wg_compute.
-template <int KB, int QN, bool GATHER, bool Z8, bool EXACT>
-__device__ __forceinline__ void wgrad_item(const WgradPlan& P, int job, int kind, int chunk,
-                                           float (*Qt)[128][kQtLd], float (*Es)[2][32]) {
+// EXACT: the exact path, with Z8 for the items whose Z is the 8-bit checkpoint.
+// Share: its LDS, or the plain path's Q tiles.
+template <int KB, int QN, bool GATHER, bool Z8, bool EXACT, class Share>
+__device__ __forceinline__ void wgrad_item(const WgradPlan& P, int job, int kind, int chunk, Share& sh) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int g = lane >> 4, cl = lane & 15;
   const int a = P.job_adapter[job];
@@ -350,10 +437,10 @@ __device__ __forceinline__ void wgrad_item(const WgradPlan& P, int job, int kind
   // covers only the set it needs.
   // (a gathered batch waits for its row indices anyway: a shallow ring)
   constexpr int D = GATHER ? 2 : kWgDepth;
-  std::conditional_t<Z8, WgRegs8<KB, QN>, WgRegs<KB, QN>> R[D];
+  std::conditional_t<EXACT, WgRegsX<KB, QN, Z8>, WgRegs<KB, QN>> R[D];
   auto load = [&](auto& Rs) {
-    if constexpr (Z8)
-      wg_load8<KB, QN, GATHER>(P, Q, ldq, rank, ccol, col_ok, chunk * (4 * 16 * QN), seg_end, lc, Rs);
+    if constexpr (EXACT)
+      wg_load_x<KB, QN, GATHER, Z8>(P, Z, ldz, ncols, Q, ldq, rank, ccol, col_ok, chunk * (4 * 16 * QN), seg_end, lc, Rs);
     else
       wg_load<KB, QN, GATHER>(P, Z, ldz, ncols, Q, ldq, rank, ccol, col_ok, seg_end, lc, Rs);
     wg_advance(P, seg_end, lc);
@@ -363,29 +450,18 @@ __device__ __forceinline__ void wgrad_item(const WgradPlan& P, int job, int kind
   for (int i = 0; i < nsteps; i += D) {
 #pragma unroll
     for (int s = 0; s < D; ++s) {
-      wg_commit_q<KB>(R[s], Qt[s]);
-      if constexpr (Z8) {
-        if (threadIdx.x < QN * 16) Es[s][threadIdx.x >> 5][threadIdx.x & 31] = q8_scale(R[s].e);
-      }
-      __syncthreads();
-      bf16x8 fa[QN];
-      if constexpr (Z8) {
-        // e4m3 times its power of two is exact in bf16
-        const float* es = &Es[s][QN == 4 ? wave >> 1 : 0][8 * g];
-        const f32x4 s0 = *reinterpret_cast<const f32x4*>(es), s1 = *reinterpret_cast<const f32x4*>(es + 4);
-        uint32_t zb[8][QN / 2];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float sc = e < 4 ? s0[e & 3] : s1[e & 3];
-          zb[e][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(R[s].z[e], sc, false));
-          if constexpr (QN == 4)
-            zb[e][QN / 2 - 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(R[s].z[e], sc, true));
-        }
-        wg_transpose<QN>(zb, fa);
+      if constexpr (EXACT) {
+        // two buffers: a wave that commits step i + 2 has passed the barrier of
+        // step i + 1, which every wave reaches behind its reads of step i
+        const int b = (i + s) & 1;
+        wg_commit_x<KB, QN, Z8>(R[s], sh, b);
+        __syncthreads();
+        wg_compute_x<KB, QN, Z8>(R[s], sh, b, acc);
       } else {
-        wg_transpose<QN>(R[s].z, fa);
+        wg_commit_q<KB, QN>(R[s], sh[s]);
+        __syncthreads();
+        wg_compute<KB, QN>(R[s], sh[s], acc);
       }
-      wg_compute<KB, QN, EXACT>(fa, Qt[s], acc);
       load(R[s]);
     }
   }
@@ -430,12 +506,11 @@ __device__ __forceinline__ void wgrad_item(const WgradPlan& P, int job, int kind
   }
 }
 
-// X8: x is an 8-bit checkpoint. Its gradients are held to the error of fp32
-// sums (three-part Q): the second part alone would leave about 3e-6.
+// X8: x is an 8-bit checkpoint.
 template <bool GATHER, bool X8>
 __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradPlan P) {
-  __shared__ alignas(16) float Qt[kWgDepth][128][kQtLd];
-  __shared__ alignas(16) float Es[X8 ? kWgDepth : 1][2][32];
+  using Share = std::conditional_t<X8, WgShareX, float[kWgDepth][128][kQtLd]>;
+  __shared__ alignas(16) Share sh;
   __shared__ int job_of_item;
   // locate the job with one parallel read of the item table (thread j checks
   // job j); items are laid out job by job, dB chunks before dA chunks
@@ -454,8 +529,8 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradPlan P) {
   const int chunk = kind == 0 ? local : local - nb_db;
   auto run = [&](auto kb) {
     constexpr int KB = decltype(kb)::value;
-    if (X8 && kind == 1) wgrad_item<KB, wgrad_qn(KB), GATHER, X8, X8>(P, job, kind, chunk, Qt, Es);
-    else wgrad_item<KB, wgrad_qn(KB), GATHER, false, X8>(P, job, kind, chunk, Qt, Es);
+    if (X8 && kind == 1) wgrad_item<KB, wgrad_qn(KB), GATHER, X8, X8>(P, job, kind, chunk, sh);
+    else wgrad_item<KB, wgrad_qn(KB), GATHER, false, X8>(P, job, kind, chunk, sh);
   };
   switch (wgrad_kb(P.job_rank[job])) {
     case 1: run(std::integral_constant<int, 1>{}); break;

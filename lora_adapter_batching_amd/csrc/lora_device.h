@@ -142,20 +142,6 @@ __device__ __forceinline__ void split8(const float (&f)[8], bf16x8& hi, bf16x8& 
   }
 }
 
-// The same in three parts (24 mantissa bits): what is left of an fp32 value is
-// nothing, or below the last bit of an fp32 sum.
-__device__ __forceinline__ void split8(const float (&f)[8], bf16x8& hi, bf16x8& mid, bf16x8& lo) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const __bf16 h = static_cast<__bf16>(f[e]);
-    const float r = f[e] - static_cast<float>(h);
-    const __bf16 m = static_cast<__bf16>(r);
-    hi[e] = h;
-    mid[e] = m;
-    lo[e] = static_cast<__bf16>(r - static_cast<float>(m));
-  }
-}
-
 // D = A(32x16) * B(16x32) + C. Lane l supplies A[l%32][8(l/32)+e] and
 // B[8(l/32)+e][l%32] (e = 0..7) and holds D[8(i/4)+4(l/32)+(i%4)][l%32].
 __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {

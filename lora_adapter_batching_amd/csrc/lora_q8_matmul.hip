@@ -114,12 +114,17 @@ __device__ __forceinline__ void tile_of(const MatArgs& a, int b, int grid, int& 
 //    registers under the matrix instructions of the current half,
 //  - the tile's exponents are fetched once, all loads in flight together (one
 //    row after the other: 407 us instead of 390).
-// Now 390 us, 2.47 PFLOP/s; the increment per step runs at 3.0, the rest is each
-// tile's start and end (11 us of 56).
+//  - its y leaves by non-temporal stores: all CUs end their tiles at about the
+//    same time, and 4 MB of y an XCD would push the rows of the next tiles out of
+//    its L2 (395 us instead of 361). Smaller tiles keep plain stores: their y
+//    is small and the next operator reads it.
+// Now 361 us, 2.66 PFLOP/s (the library's fp8 product without block scales: 384).
+// The steps run at 3.0; the rest is each tile's start and end (6 us of 52).
 // ---------------------------------------------------------------------------
-template <int BT_, int BN_, int WT_, int WN_, int S_, int KS_ = 1>
+template <int BT_, int BN_, int WT_, int WN_, int S_, int KS_ = 1, bool STREAM_ = false>
 struct Tile {
   static constexpr int BT = BT_, BN = BN_, WT = WT_, WN = WN_, S = S_, KS = KS_;
+  static constexpr bool STREAM = STREAM_;               // y goes past the caches
   static constexpr int waves = WT * WN;                 // of one group; KS groups share the sum
   static constexpr int TT = BT / WT, TN = BN / WN;      // a wave's tokens and columns
   static constexpr int FT = TT / 32, FN = TN / 32;      // its fragments
@@ -361,9 +366,30 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
           }
   }
   // Epilogue through LDS, so that a row's columns leave in whole lines:
-  // 32 tokens at a time in fp32, 8 columns per lane back.
+  // 32 tokens at a time in fp32, 8 columns per lane back. What is added to is
+  // read a group of tokens ahead (loads and stores of the same matrix are kept
+  // in program order, so a load behind a store would wait its whole latency).
   uint8_t* ep = smem + C::parts + wave * 32 * C::eprow;
   constexpr int LPR = C::TN / 8;        // lanes per row
+  constexpr int NP = LPR / 2;           // passes over 32 LPR pieces of 8 columns
+  auto place = [&](int i, int p, int& r, int& c, uint16_t*& yp) -> bool {
+    r = (64 * p + lane) / LPR;
+    c = (64 * p + lane) % LPR;
+    const int t = t0 + wt * C::TT + 32 * i + r, ncol = ncol0 + 8 * c;
+    yp = a.y + (int64_t)t * a.ldy + ncol;
+    return t < a.T && ncol < a.N;
+  };
+  u32x4 old[2][ADD ? NP : 1];
+  auto fetch = [&](int i) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      int r, c;
+      uint16_t* yp;
+      old[i & 1][p] = zero16();
+      if (place(i, p, r, c, yp)) old[i & 1][p] = ld16(yp);
+    }
+  };
+  if constexpr (ADD) fetch(0);
 #pragma unroll
   for (int i = 0; i < C::FT; ++i) {
 #pragma unroll
@@ -373,23 +399,25 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
         f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         *reinterpret_cast<f32x4*>(ep + m * C::eprow + (32 * j + 8 * q + 4 * h) * 4) = v;
       }
+    if constexpr (ADD)
+      if (i + 1 < C::FT) fetch(i + 1);
 #pragma unroll
-    for (int p = 0; p < LPR / 2; ++p) {  // 32 LPR pieces of 8 columns
-      const int r = (64 * p + lane) / LPR, c = (64 * p + lane) % LPR;
-      const int t = t0 + wt * C::TT + 32 * i + r;
-      const int ncol = ncol0 + 8 * c;
+    for (int p = 0; p < NP; ++p) {
+      int r, c;
+      uint16_t* yp;
+      const bool in = place(i, p, r, c, yp);
       const f32x4 v0 = *reinterpret_cast<const f32x4*>(ep + r * C::eprow + c * 32);
       const f32x4 v1 = *reinterpret_cast<const f32x4*>(ep + r * C::eprow + c * 32 + 16);
-      if (t < a.T && ncol < a.N) {
-        uint16_t* yp = a.y + (int64_t)t * a.ldy + ncol;
-        float f[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
-        if constexpr (ADD) {
-          float o[8];
-          unpack8(ld16(yp), o);
+      float f[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+      if constexpr (ADD) {
+        float o[8];
+        unpack8(old[i & 1][p], o);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] += o[e];
-        }
-        st16(yp, pack8(f));
+        for (int e = 0; e < 8; ++e) f[e] += o[e];
+      }
+      if (in) {
+        if constexpr (C::STREAM) __builtin_nontemporal_store(pack8(f), reinterpret_cast<u32x4*>(yp));
+        else st16(yp, pack8(f));
       }
     }
   }
@@ -508,7 +536,7 @@ struct TileChoice {
   void (*launch)(MatArgs, bool, hipStream_t);
 };
 const TileChoice kTiles[] = {
-    {256, 256, 1, 256, 11.6f, 1.40f, launch_tile<Tile<256, 256, 2, 2, 2>>},
+    {256, 256, 1, 256, 11.6f, 1.40f, launch_tile<Tile<256, 256, 2, 2, 2, 1, true>>},
     {128, 128, 1, 512, 2.8f, 1.00f, launch_tile<Tile<128, 128, 2, 2, 2>>},
     {128, 128, 1, 256, 6.9f, 0.34f, launch_tile<Tile<128, 128, 2, 2, 3>>},
     {128, 160, 1, 256, 8.5f, 0.37f, launch_tile<Tile<128, 160, 4, 1, 3>>},
