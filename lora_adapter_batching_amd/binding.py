@@ -66,6 +66,7 @@ EXPORTS = ["lora_segments_from_ids", "lora_workspace_size", "lora_sgmv_shrink", 
 NOALLOC_SCRATCH_BYTES = 16 << 20  # LORA_NOALLOC_SCRATCH_BYTES
 
 _lib = None
+_torch = None  # set by load(): the hot calls look it up once per call, not per import statement
 
 
 def load(path: str = LIB_PATH):
@@ -78,7 +79,9 @@ def load(path: str = LIB_PATH):
     # torch (which provides the device memory and streams) brings its own HIP
     # runtime; loading it first makes the library bind to that same runtime,
     # so that one HIP runtime serves the process
-    import torch  # noqa: F401
+    import torch
+    global _torch
+    _torch = torch
     lib = ctypes.CDLL(path)
     P = ctypes.c_void_p
     I64 = ctypes.c_int64
@@ -446,11 +449,12 @@ def new_q8_weights(rows: int, width: int, device="cuda") -> Q8Weights:
 
 def _rows_arg(name: str, t, rows: int, width: int, dev: int) -> int:
     """The row stride of a bfloat16 [>= rows, width] tensor on GPU `dev`."""
-    import torch
-    if t.dtype is torch.bfloat16 and t.get_device() == dev:
-        shape, stride = t.shape, t.stride()
-        if len(shape) == 2 and shape[0] >= rows and shape[1] == width and stride[1] == 1:
-            return stride[0]
+    if t.dtype is _torch.bfloat16 and t.get_device() == dev:
+        shape = t.shape
+        if len(shape) == 2 and shape[0] >= rows and shape[1] == width:
+            stride, step = t.stride()
+            if step == 1:
+                return stride
     raise ValueError(f"{name} must be a bfloat16 [>= {rows}, {width}] matrix with unit column stride on "
                      f"{_dev_name(dev)}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
@@ -469,13 +473,13 @@ def _call_on(dev: int, stream, fn, *args):
     """Calls fn(*args, stream) with GPU `dev` current, on `stream` or that
     GPU's current stream. (A decode step makes many such calls and each is a
     few microseconds of GPU work, so the host's share is kept small.)"""
-    import torch
     if dev < 0:
         raise ValueError("device tensors are needed, got cpu")
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
+    cuda = _torch._C
+    if dev != cuda._cuda_getDevice():
+        with _torch.cuda.device(dev):
             return _call_on(dev, stream, fn, *args)
-    st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream))
+    st = fn(*args, cuda._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream))
     if st:
         _check(st)
 
@@ -483,23 +487,24 @@ def _call_on(dev: int, stream, fn, *args):
 def q8_quantize(x, out: _Q8, out_t: Optional[Q8Weights] = None, stream=None):
     """Stores bf16 x in 8 bits (Q8Rows or Q8Weights); with out_t the
     transposed weights too."""
-    dev = out.dev
+    lib, dev = _lib or load(), out.dev
     ldx = _rows_arg("x", x, out.rows, out.width, dev)
     ot = _q8_arg("out_t", out_t, dev) if out_t is not None else None
-    _call_on(dev, stream, (_lib or load()).lora_q8_quantize, x.data_ptr(), ldx, out.addr, ot)
+    _call_on(dev, stream, lib.lora_q8_quantize, x.data_ptr(), ldx, out.addr, ot)
 
 
 def q8_dequantize(q: _Q8, x, stream=None):
     """Restores an 8-bit matrix to bf16 x."""
+    lib = _lib or load()
     ldx = _rows_arg("x", x, q.rows, q.width, q.dev)
-    _call_on(q.dev, stream, (_lib or load()).lora_q8_dequantize, q.addr, x.data_ptr(), ldx)
+    _call_on(q.dev, stream, lib.lora_q8_dequantize, q.addr, x.data_ptr(), ldx)
 
 
 def q8_matmul(x: Q8Rows, w: Q8Weights, y, accumulate: bool = False, stream=None):
     """y = x w^T (or y += x w^T) on 8-bit operands; y bf16 [x.rows, w.rows]."""
-    dev = x.dev
+    lib, dev = _lib or load(), x.dev
     ldy = _rows_arg("y", y, x.rows, w.rows, dev)
-    _call_on(dev, stream, (_lib or load()).lora_q8_matmul, x.addr, _q8_arg("w", w, dev), y.data_ptr(), ldy,
+    _call_on(dev, stream, lib.lora_q8_matmul, x.addr, _q8_arg("w", w, dev), y.data_ptr(), ldy,
              1 if accumulate else 0)
 
 
@@ -507,37 +512,37 @@ def packed_backward_q8(x: Q8Rows, dy, u, adapters: Adapters, segments: Segments,
                        flags: int = 0, ws=None, stream=None):
     """packed_backward with x as the 8-bit checkpoint; u (the forward's
     u_save) is required."""
-    T, dev = segments.num_tokens, x.dev
+    lib, T, dev = _lib or load(), segments.num_tokens, x.dev
     lddy = _rows_arg("dy", dy, T, adapters.h_out, dev)
     lddx = _rows_arg("dx", dx, T, adapters.h_in, dev) if dx is not None else 0
     if u is None or u.get_device() != dev or u.dim() != 2 or u.shape[0] < T or u.stride(1) != 1 or u.element_size() != 4:
         raise ValueError(f"u must be a float32 [>= {T}, >= largest rank] matrix with unit column stride on {_dev_name(dev)}")
     wp, wb = _ws(ws)
-    _call_on(dev, stream, (_lib or load()).lora_packed_backward_q8, x.addr, dy.data_ptr(), lddy, u.data_ptr(),
+    _call_on(dev, stream, lib.lora_packed_backward_q8, x.addr, dy.data_ptr(), lddy, u.data_ptr(),
              u.stride(0), adapters.c, segments.c, _ptr(dx), lddx, _ptr(dA_ptrs), _ptr(dB_ptrs), int(flags), wp, wb)
 
 
 def swiglu(gate_up, h=None, hq: Optional[Q8Rows] = None, stream=None):
     """h = silu(gate) * up of gate_up [T, 2F], as bf16 rows and/or 8-bit rows."""
+    lib, dev = _lib or load(), gate_up.get_device()
     T, W = gate_up.shape
-    dev = gate_up.get_device()
     F = W // 2
     ld = _rows_arg("gate_up", gate_up, T, 2 * F, dev)
     ldh = _rows_arg("h", h, T, F, dev) if h is not None else 0
     q = _q8_arg("hq", hq, dev) if hq is not None else None
-    _call_on(dev, stream, (_lib or load()).lora_swiglu, gate_up.data_ptr(), ld, T, F, _ptr(h), ldh, q)
+    _call_on(dev, stream, lib.lora_swiglu, gate_up.data_ptr(), ld, T, F, _ptr(h), ldh, q)
 
 
 def swiglu_backward(gate_up, dh, dgate_up=None, dgate_up_q: Optional[Q8Rows] = None, stream=None):
     """The gradient of swiglu's input, [T, 2F], as bf16 rows and/or 8-bit rows."""
+    lib, dev = _lib or load(), gate_up.get_device()
     T, W = gate_up.shape
-    dev = gate_up.get_device()
     F = W // 2
     ld = _rows_arg("gate_up", gate_up, T, 2 * F, dev)
     lddh = _rows_arg("dh", dh, T, F, dev)
     ldd = _rows_arg("dgate_up", dgate_up, T, 2 * F, dev) if dgate_up is not None else 0
     q = _q8_arg("dgate_up_q", dgate_up_q, dev) if dgate_up_q is not None else None
-    _call_on(dev, stream, (_lib or load()).lora_swiglu_backward, gate_up.data_ptr(), ld, dh.data_ptr(), lddh, T, F,
+    _call_on(dev, stream, lib.lora_swiglu_backward, gate_up.data_ptr(), ld, dh.data_ptr(), lddh, T, F,
              _ptr(dgate_up), ldd, q)
 
 

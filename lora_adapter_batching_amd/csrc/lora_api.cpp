@@ -746,6 +746,7 @@ int set_error(int status, const char* fmt, ...) {
   g_last_error = buf;
   return status;
 }
+void clear_error() { g_last_error.clear(); }
 }  // namespace lora
 
 // ===========================================================================

@@ -26,5 +26,7 @@ int sgmv_fused_from(const void* x, int64_t ldx, const lora_adapters_t* adapters,
 
 // Sets the calling thread's lora_last_error() text; returns `status`.
 int set_error(int status, const char* fmt, ...);
+// Empties it (every entry point begins so).
+void clear_error();
 
 }  // namespace lora

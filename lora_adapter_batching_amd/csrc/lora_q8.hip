@@ -413,7 +413,7 @@ int check_q8(const lora_q8_t* q, const char* name, int block_rows) {
 using namespace lora;
 
 extern "C" int lora_q8_quantize(const void* x, int64_t ldx, const lora_q8_t* out, const lora_q8_t* out_t, void* stream) {
-  set_error(LORA_OK, "%s", "");
+  clear_error();
   int st = check_q8(out, "out", 0);
   if (st) return st;
   if (out_t) {
@@ -456,7 +456,7 @@ extern "C" int lora_q8_quantize(const void* x, int64_t ldx, const lora_q8_t* out
 }
 
 extern "C" int lora_q8_dequantize(const lora_q8_t* q, void* x, int64_t ldx, void* stream) {
-  set_error(LORA_OK, "%s", "");
+  clear_error();
   int st = check_q8(q, "q", 0);
   if (st) return st;
   if (q->rows == 0) return LORA_OK;
@@ -500,7 +500,7 @@ static int gate_checks(const void* gate_up, int64_t ld, int32_t tokens, int32_t 
 
 extern "C" int lora_swiglu(const void* gate_up, int64_t ld, int32_t num_tokens, int32_t width, void* h, int64_t ldh,
                            const lora_q8_t* hq, void* stream) {
-  set_error(LORA_OK, "%s", "");
+  clear_error();
   int st = gate_checks(gate_up, ld, num_tokens, width, h, ldh, hq, width, "h", "hq");
   if (st || num_tokens == 0) return st;
   GateArgs a{};
@@ -529,7 +529,7 @@ extern "C" int lora_swiglu(const void* gate_up, int64_t ld, int32_t num_tokens, 
 
 extern "C" int lora_swiglu_backward(const void* gate_up, int64_t ld, const void* dh, int64_t lddh, int32_t num_tokens,
                                     int32_t width, void* dgate_up, int64_t lddg, const lora_q8_t* dgate_up_q, void* stream) {
-  set_error(LORA_OK, "%s", "");
+  clear_error();
   int st = gate_checks(gate_up, ld, num_tokens, width, dgate_up, lddg, dgate_up_q, 2 * (int64_t)width, "dgate_up", "dgate_up_q");
   if (st || num_tokens == 0) return st;
   if ((st = check_bf16_rows(dh, lddh, width, "dh"))) return st;

@@ -74,6 +74,11 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// Where the waves that share a ring meet: a ring of one wave needs no barrier.
+template <int WAVES>
+__device__ __forceinline__ void ring_barrier() {
+  if constexpr (WAVES > 1) __builtin_amdgcn_s_barrier();
+}
 
 // Tile of workgroup b: each XCD (b % 8) takes a contiguous run of the tiles,
 // ordered in groups of kGroupT token tiles, so that the tiles an XCD's CUs
@@ -116,10 +121,10 @@ __device__ __forceinline__ void tile_of(const MatArgs& a, int b, int grid, int& 
 //    row after the other: 407 us instead of 390).
 //  - its y leaves by non-temporal stores: all CUs end their tiles at about the
 //    same time, and 4 MB of y an XCD would push the rows of the next tiles out of
-//    its L2 (395 us instead of 361). Smaller tiles keep plain stores: their y
+//    its L2 (395 us without). Smaller tiles keep plain stores: their y
 //    is small and the next operator reads it.
-// Now 361 us, 2.66 PFLOP/s (the library's fp8 product without block scales: 384).
-// The steps run at 3.0; the rest is each tile's start and end (6 us of 52).
+// Now 361-371 us, 2.6 PFLOP/s (the library's fp8 product without block scales:
+// 384). The steps run at 3.0; the rest is each tile's start and end (6 us of 52).
 // ---------------------------------------------------------------------------
 template <int BT_, int BN_, int WT_, int WN_, int S_, int KS_ = 1, bool STREAM_ = false>
 struct Tile {
@@ -296,7 +301,7 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
   }
   wait_vm<(C::S - 1) * C::loads>();
   wait_lds();
-  __builtin_amdgcn_s_barrier();
+  ring_barrier<C::waves>();
 #pragma unroll
   for (int j = 0; j < C::FN; ++j) fw[0][j] = read_frag(0, 0, wrow + 32 * j);
 #pragma unroll
@@ -308,7 +313,7 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
       load_exps(kb0, ev);
       store_exps(ev);
       wait_lds();
-      __builtin_amdgcn_s_barrier();
+      ring_barrier<C::waves>();
     }
     Exps raw;
     read_exps(kb0, kb0, raw);
@@ -320,14 +325,14 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
       // be in flight); the barrier makes both true for every wave
       wait_vm<(C::S - 2) * C::loads>();
       wait_lds();
-      __builtin_amdgcn_s_barrier();
+      ring_barrier<C::waves>();
       __builtin_amdgcn_sched_barrier(0);
       half(std::integral_constant<int, 1>{}, e, i, kb0, raw);
       e = shift_exps(k0 + i + 1, raw);
     }
     // the exponents are refilled only when every wave has read its last ones
     wait_lds();
-    __builtin_amdgcn_s_barrier();
+    ring_barrier<C::waves>();
   }
   // The last steps' empty loads write LDS too: they end, in every wave, before
   // it is used for anything else.
@@ -367,8 +372,9 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
   }
   // Epilogue through LDS, so that a row's columns leave in whole lines:
   // 32 tokens at a time in fp32, 8 columns per lane back. What is added to is
-  // read a group of tokens ahead (loads and stores of the same matrix are kept
-  // in program order, so a load behind a store would wait its whole latency).
+  // read before the first store, into the registers that the fragments leave
+  // free: loads and stores of the same matrix are kept in program order, and a
+  // load behind a store would wait its whole latency.
   uint8_t* ep = smem + C::parts + wave * 32 * C::eprow;
   constexpr int LPR = C::TN / 8;        // lanes per row
   constexpr int NP = LPR / 2;           // passes over 32 LPR pieces of 8 columns
@@ -379,17 +385,18 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
     yp = a.y + (int64_t)t * a.ldy + ncol;
     return t < a.T && ncol < a.N;
   };
-  u32x4 old[2][ADD ? NP : 1];
-  auto fetch = [&](int i) {
+  u32x4 old[C::FT][ADD ? NP : 1];
+  if constexpr (ADD) {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      int r, c;
-      uint16_t* yp;
-      old[i & 1][p] = zero16();
-      if (place(i, p, r, c, yp)) old[i & 1][p] = ld16(yp);
-    }
-  };
-  if constexpr (ADD) fetch(0);
+    for (int i = 0; i < C::FT; ++i)
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        int r, c;
+        uint16_t* yp;
+        old[i][p] = zero16();
+        if (place(i, p, r, c, yp)) old[i][p] = ld16(yp);
+      }
+  }
 #pragma unroll
   for (int i = 0; i < C::FT; ++i) {
 #pragma unroll
@@ -399,8 +406,6 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
         f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         *reinterpret_cast<f32x4*>(ep + m * C::eprow + (32 * j + 8 * q + 4 * h) * 4) = v;
       }
-    if constexpr (ADD)
-      if (i + 1 < C::FT) fetch(i + 1);
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       int r, c;
@@ -411,7 +416,7 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
       float f[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
       if constexpr (ADD) {
         float o[8];
-        unpack8(old[i & 1][p], o);
+        unpack8(old[i][p], o);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] += o[e];
       }
@@ -425,62 +430,45 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
 
 // ---------------------------------------------------------------------------
 // Few tokens: the weights are read once and that is the floor. A workgroup
-// owns 16 columns and up to 16 TF tokens; its 8 waves take every eighth block
-// of the sum straight from memory into fragments (no LDS on the way, each w
-// row in whole 128-byte lines) and their parts are added in wave order.
+// owns 16 columns and up to 16 tokens; its 8 waves take every eighth block of
+// the sum straight from memory into fragments (no LDS on the way, each w row in
+// whole 128-byte lines) and their parts are added in wave order. Eight small
+// workgroups a CU hide the latency: two to four blocks in flight per wave, or
+// 16 waves, were no faster. One token 2560 -> 2560 4.0 us, 2560 -> 19456 10.9 us
+// (4.6 TB/s), 9728 -> 2560 8.6 us.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
-constexpr int kFewDepth = 2;  // blocks whose loads a wave has in flight
+constexpr int kFewTokens = 16;
 
-template <int TF, bool ADD>
+template <bool ADD>
 __global__ __launch_bounds__(64 * kFewWaves) void q8_few_kernel(MatArgs a) {
-  __shared__ alignas(16) float part[kFewWaves][TF * 16][16 + 4];
+  __shared__ alignas(16) float part[kFewWaves][kFewTokens][16 + 4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16, t0 = blockIdx.y * (16 * TF);
-  const int vn = min(16, a.N - n0), vt = min(16 * TF, a.T - t0);
+  const int n0 = blockIdx.x * 16;
+  const int vn = min(16, a.N - n0), vt = a.T;
   const int64_t kbytes = (int64_t)a.nkb * 128;
   const __amdgpu_buffer_rsrc_t wr = mk_rsrc(a.w + (int64_t)n0 * a.ldw, (int64_t)(vn - 1) * a.ldw + kbytes);
-  const __amdgpu_buffer_rsrc_t xr = mk_rsrc(a.x + (int64_t)t0 * a.ldx, (int64_t)(vt - 1) * a.ldx + kbytes);
-  const __amdgpu_buffer_rsrc_t xer = mk_rsrc(a.xe + (int64_t)t0 * a.ldxe, (int64_t)(vt - 1) * a.ldxe + a.nkb);
+  const __amdgpu_buffer_rsrc_t xr = mk_rsrc(a.x, (int64_t)(vt - 1) * a.ldx + kbytes);
+  const __amdgpu_buffer_rsrc_t xer = mk_rsrc(a.xe, (int64_t)(vt - 1) * a.ldxe + a.nkb);
   const __amdgpu_buffer_rsrc_t wer = mk_rsrc(a.we + (int64_t)(n0 >> 7) * a.ldwe, a.nkb);
-  f32x4 acc[TF];
-#pragma unroll
-  for (int f = 0; f < TF; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int kb0 = wave; kb0 < a.nkb; kb0 += kFewWaves * kFewDepth) {
-    u32x4 w[kFewDepth][2], x[kFewDepth][TF][2];
-    int ew[kFewDepth], ex[kFewDepth][TF];
-#pragma unroll
-    for (int d = 0; d < kFewDepth; ++d) {
-      const int kb = kb0 + d * kFewWaves;
-      const bool in = kb < a.nkb;
-      const uint32_t k = (uint32_t)kb * 128u + 32u * g;
-      const uint32_t wo = in ? (uint32_t)((int64_t)r * a.ldw) + k : kOff;
-      w[d][0] = bld16(wr, wo);
-      w[d][1] = bld16(wr, wo + 16);
-      ew[d] = __builtin_amdgcn_raw_buffer_load_b8(wer, in ? kb : (int)kOff, 0, 0);
-#pragma unroll
-      for (int f = 0; f < TF; ++f) {
-        const uint32_t xo = in && 16 * f + r < vt ? (uint32_t)((int64_t)(16 * f + r) * a.ldx) + k : kOff;
-        x[d][f][0] = bld16(xr, xo);
-        x[d][f][1] = bld16(xr, xo + 16);
-        ex[d][f] = __builtin_amdgcn_raw_buffer_load_b8(
-            xer, in && 16 * f + r < vt ? (int)((int64_t)(16 * f + r) * a.ldxe) + kb : (int)kOff, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int d = 0; d < kFewDepth; ++d)
-#pragma unroll
-      for (int f = 0; f < TF; ++f)
-        acc[f] = mfma8_16(frag(w[d][0], w[d][1]), frag(x[d][f][0], x[d][f][1]), acc[f], ew[d], ex[d][f]);
+  const bool row = r < vt;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int kb = wave; kb < a.nkb; kb += kFewWaves) {
+    const uint32_t k = (uint32_t)kb * 128u + 32u * g;
+    const uint32_t wo = (uint32_t)((int64_t)r * a.ldw) + k;
+    const uint32_t xo = row ? (uint32_t)((int64_t)r * a.ldx) + k : kOff;
+    const u32x4 w0 = bld16(wr, wo), w1 = bld16(wr, wo + 16);
+    const u32x4 x0 = bld16(xr, xo), x1 = bld16(xr, xo + 16);
+    const int ew = __builtin_amdgcn_raw_buffer_load_b8(wer, kb, 0, 0);
+    const int ex = __builtin_amdgcn_raw_buffer_load_b8(xer, row ? (int)((int64_t)r * a.ldxe) + kb : (int)kOff, 0, 0);
+    acc = mfma8_16(frag(w0, w1), frag(x0, x1), acc, ew, ex);
   }
-#pragma unroll
-  for (int f = 0; f < TF; ++f) *reinterpret_cast<f32x4*>(&part[wave][16 * f + r][4 * g]) = acc[f];
+  *reinterpret_cast<f32x4*>(&part[wave][r][4 * g]) = acc;
   __syncthreads();
-  for (int i = threadIdx.x; i < TF * 32; i += 64 * kFewWaves) {
-    const int t = i >> 1, c = (i & 1) * 8;
-    if (t >= vt || n0 + c >= a.N) continue;
+  const int t = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
+  if (t < vt && n0 + c < a.N) {
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = 0.f;
@@ -488,7 +476,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void q8_few_kernel(MatArgs a) {
     for (int wv = 0; wv < kFewWaves; ++wv)
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] += part[wv][t][c + e];
-    uint16_t* yp = a.y + (int64_t)(t0 + t) * a.ldy + n0 + c;
+    uint16_t* yp = a.y + (int64_t)t * a.ldy + n0 + c;
     if constexpr (ADD) {
       float o[8];
       unpack8(ld16(yp), o);
@@ -508,11 +496,10 @@ void launch_tile(MatArgs a, bool add, hipStream_t s) {
   else hipLaunchKernelGGL((q8_tile_kernel<C, false>), grid, blk, 0, s, a);
 }
 
-template <int TF>
 void launch_few(const MatArgs& a, bool add, hipStream_t s) {
-  const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.T + 16 * TF - 1) / (16 * TF))), blk(64 * kFewWaves);
-  if (add) hipLaunchKernelGGL((q8_few_kernel<TF, true>), grid, blk, 0, s, a);
-  else hipLaunchKernelGGL((q8_few_kernel<TF, false>), grid, blk, 0, s, a);
+  const dim3 grid((unsigned)((a.N + 15) / 16)), blk(64 * kFewWaves);
+  if (add) hipLaunchKernelGGL(q8_few_kernel<true>, grid, blk, 0, s, a);
+  else hipLaunchKernelGGL(q8_few_kernel<false>, grid, blk, 0, s, a);
 }
 
 // Tiles to choose from. A workgroup of a tile takes about fixed + step * (its
@@ -520,15 +507,17 @@ void launch_few(const MatArgs& a, bool add, hipStream_t s) {
 // that times the rounds its tiles need. Measured on 256 CUs (us; the sum is n
 // blocks long): the largest tile has the best rate and needs the most of
 // them, the small ones fill the GPU where there are few tokens.
-//   tokens, k, n            256x256  128x128  128x128*  128x160  128x96  128x64  32x64  32x32
-//   8191, 4096, 4096            120      138       160      159     181     220
-//   2048, 4096, 4096             45       35        40
-//   1024, 4096, 4096                      27        21       22      31      30
-//   256, 2560, 19456             35       23        27       18      24      30     68    122
-//   128, 2560, 19456                      20        15       16      13      21     35     65
-//   512, 2560, 2560                       18        14       15      12      11     22     33
-//   100, 9728, 2560                       51        32                       25     15     23
-//   37, 9728, 2560                        48        31                       24     15     12
+//   tokens, k, n        256x256  128x128  128x128*  128x160  128x96  128x64  32x64  32x32
+//   8192, 4096, 14336       367      451
+//   8191, 4096, 4096        109      131       160      159     181     220
+//   2048, 4096, 4096         45       35        40
+//   1024, 4096, 4096                  27        21       22      31      30
+//   256, 2560, 19456         35       23        27       19      24      30     69    107
+//   128, 2560, 19456                  20        15       16      14      21     35     58
+//   512, 2560, 2560                   19        14       15      12      11     22     31
+//   128, 2560, 2560                   17        13       14      12      10      8     12
+//   100, 9728, 2560                   51        32       38      30      25     15     21
+//   37, 9728, 2560                    48        31       37      30      25     15     12
 // (* with three stages, one workgroup per CU; the other holds two)
 struct TileChoice {
   int bt, bn, ks, slots;
@@ -543,14 +532,15 @@ const TileChoice kTiles[] = {
     {128, 96, 1, 256, 7.0f, 0.26f, launch_tile<Tile<128, 96, 4, 1, 3>>},
     {128, 64, 1, 256, 5.4f, 0.26f, launch_tile<Tile<128, 64, 2, 2, 3>>},
     {32, 64, 4, 256, 4.0f, 0.56f, launch_tile<Tile<32, 64, 1, 2, 3, 4>>},
-    {32, 32, 6, 256, 3.8f, 0.65f, launch_tile<Tile<32, 32, 1, 1, 3, 6>>},
+    {32, 32, 4, 256, 4.2f, 0.39f, launch_tile<Tile<32, 32, 1, 1, 4, 4>>},
 };
 
 void launch_matmul(const MatArgs& a, bool add, hipStream_t s) {
-  // One matrix fragment of tokens: the weights' bytes are all that counts (16
-  // tokens, 2560 -> 19456: 15 us against 18 with 32 x 64 tiles; 9728 -> 2560: 12
-  // against 12; one token 11 against 17 and 9 against 11).
-  if (a.T <= 16) return launch_few<1>(a, add, s);
+  // One matrix fragment of tokens: the weights' bytes are all that counts (one
+  // token 2560 -> 2560: 4.0 us against 6.2 with 32 x 32 tiles, 2560 -> 19456: 11
+  // against 13 with 128 x 96; 16 tokens 4.9 against 6.2 and 15 against 13, 9728 ->
+  // 2560: 12 either way).
+  if (a.T <= kFewTokens) return launch_few(a, add, s);
   const TileChoice* best = &kTiles[0];  // (its grid is checked by the caller)
   double least = 0.;
   for (const TileChoice& c : kTiles) {
@@ -568,7 +558,7 @@ void launch_matmul(const MatArgs& a, bool add, hipStream_t s) {
 using namespace lora;
 
 extern "C" int lora_q8_matmul(const lora_q8_t* x, const lora_q8_t* w, void* y, int64_t ldy, uint32_t flags, void* stream) {
-  set_error(LORA_OK, "%s", "");
+  clear_error();
   int st;
   if ((st = check_q8(x, "x", 1))) return st;
   if ((st = check_q8(w, "w", kQ8Block))) return st;
