@@ -58,12 +58,20 @@ __device__ __forceinline__ f32x4 mfma8_16(i32x8 a, i32x8 b, f32x4 c, int ea, int
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, ea, 0, eb);
 }
 
-// LDS-destination load whose k position is a scalar offset. The descriptor
+// LDS-destination loads whose k position is a scalar offset. The descriptor
 // ends with the last valid row; rows behind it have vector offsets past its
 // end (with or without the scalar offset counted) and write zeros.
 __device__ __forceinline__ void load_lds16_at(i32x4 rsrc, uint32_t lds_addr, uint32_t voff, uint32_t soff) {
   int m0_out;
   asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds"
+               : "={m0}"(m0_out)
+               : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
+               : "memory");
+  (void)m0_out;
+}
+__device__ __forceinline__ void load_lds4_at(i32x4 rsrc, uint32_t lds_addr, uint32_t voff, uint32_t soff) {
+  int m0_out;
+  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dword %2, %3, %4 offen lds"
                : "={m0}"(m0_out)
                : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
                : "memory");
@@ -117,8 +125,8 @@ __device__ __forceinline__ void tile_of(const MatArgs& a, int b, int grid, int& 
 //    the stages took 1.5 times as long to load (439 us),
 //  - the fragments of the next half step are read from LDS into a second set of
 //    registers under the matrix instructions of the current half,
-//  - the tile's exponents are fetched once, all loads in flight together (one
-//    row after the other: 407 us instead of 390).
+//  - the tile's exponents are fetched once, in the same way and ahead of the
+//    first stage (through registers, row after row: 407 us instead of 390).
 //  - its y leaves by non-temporal stores: all CUs end their tiles at about the
 //    same time, and 4 MB of y an XCD would push the rows of the next tiles out of
 //    its L2 (395 us without). Smaller tiles keep plain stores: their y
@@ -142,20 +150,24 @@ struct Tile {
   static constexpr int erows = BT + (EW == 1 ? (BN + 127) / 128 : (BN + 254) / 128);  // exponent rows: tokens, w blocks
   static constexpr int ring = S * stage;                // one group's stages
   static constexpr int eoff = KS * ring;
-  static constexpr int egrp = erows * 17 * 4;           // one group's exponents
+  static constexpr int eloads = (erows + 4 * waves - 1) / (4 * waves);  // 256 bytes (4 rows) each, per wave
+  static constexpr int egrp = eloads * waves * 256;     // one group's exponents
   static constexpr int eprow = TN * 4 + 16;             // epilogue row of one token (fp32, padded)
   static constexpr int parts = (KS - 1) * BT * BN * 4;  // the other groups' sums
   static constexpr int epi = parts + waves * 32 * eprow;
   static constexpr int used = eoff + KS * egrp;
   static constexpr int lds = used > epi ? used : epi;
+  // the first wloads (xrows) loads of every wave are w rows (token exponents)
+  static constexpr int wloads = BN / 8 / waves, xrows = BT / 4 / waves;
+  static_assert(BN % (8 * waves) == 0 && BT % (4 * waves) == 0, "no load mixes the two operands");
   static_assert(stage % (1024 * waves) == 0 && TT % 32 == 0 && TN % 32 == 0, "whole loads and fragments");
   static_assert(FT + FN <= per * FT * FN, "every fragment of the next half is read");
   static_assert(S >= 2 && lds <= 160 * 1024, "fits the LDS");
 };
 
-// Exponents in LDS: rows of 17 dwords (16 with four blocks each, one of
-// padding against bank conflicts), refilled every kExpBlocks blocks (the first
-// dword may begin up to three blocks earlier).
+// Exponents in LDS: rows of 16 dwords of four blocks each, dword d of row r at
+// position d ^ (r / 4) % 16 (the bank of a wave's 32 rows then differs), refilled
+// every kExpBlocks blocks (the first dword may begin up to three blocks earlier).
 constexpr int kExpBlocks = 60;
 
 __device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
@@ -185,7 +197,7 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
   for (int p = 0; p < C::loads; ++p) {
     const int r = 8 * (p * C::waves + wave) + (lane >> 3);
     const int c = (lane & 7) ^ swizzle(r);
-    const bool isx = 8 * (p * C::waves + wave) >= C::BN;
+    const bool isx = p >= C::wloads;
     voff[p] = (uint32_t)(isx ? (int64_t)(r - C::BN) * a.ldx : (int64_t)r * a.ldw) + 16u * c;
   }
   uint8_t* const ring = smem + grp * C::ring;
@@ -195,32 +207,26 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
   // number without a branch between them.
   auto load = [&](int kb, int slot, int p) {
     const int piece = p * C::waves + wave;
-    i32x4 r = 8 * piece >= C::BN ? xr : wr;
+    i32x4 r = p >= C::wloads ? xr : wr;
     r[2] = kb < k1 ? r[2] : 0;
     load_lds16_at(r, ring0 + (uint32_t)(slot * C::stage + piece * 1024), voff[p], (uint32_t)kb * 128u);
   };
 
-  uint32_t* const es = reinterpret_cast<uint32_t*>(smem + C::eoff + grp * C::egrp);
   const int eb0 = n0 >> 7, vb = ((n0 + vn - 1) >> 7) - eb0 + 1;
-  // The dwords with blocks kb0 .. of the group: 16 lanes per row, all loads in
-  // flight before the first is stored.
-  constexpr int EP = (C::erows + 4 * C::waves - 1) / (4 * C::waves);
-  auto load_exps = [&](int kb0, uint32_t (&v)[EP]) {
-    const int b = (kb0 & ~3) + 4 * (tid & 15);
+  const uint32_t* const es = reinterpret_cast<const uint32_t*>(smem + C::eoff + grp * C::egrp);
+  const uint32_t es0 = lds0 + (uint32_t)(C::eoff + grp * C::egrp);
+  // Loads the dwords with blocks kb0 .. of the group. What lies behind a row's
+  // last block is never used (shift_exps).
+  auto load_exps = [&](int kb0) {
+    const int dwords = (a.nkb + 3) >> 2;
+    const i32x4 xer = mk_rsrc_words(a.xe + (int64_t)t0 * a.ldxe, (int64_t)(vt - 1) * a.ldxe + 4 * dwords);
+    const i32x4 wer = mk_rsrc_words(a.we + (int64_t)eb0 * a.ldwe, (int64_t)(vb - 1) * a.ldwe + 4 * dwords);
 #pragma unroll
-    for (int p = 0; p < EP; ++p) {
-      const int r = (tid >> 4) + p * 4 * C::waves;
-      const bool isx = r < C::BT;
-      const bool ok = b < k1 && (isx ? r < vt : r - C::BT < vb);
-      const uint8_t* src = isx ? a.xe + (int64_t)(t0 + r) * a.ldxe : a.we + (int64_t)(eb0 + r - C::BT) * a.ldwe;
-      v[p] = ok ? *reinterpret_cast<const uint32_t*>(src + b) : 0u;
-    }
-  };
-  auto store_exps = [&](const uint32_t (&v)[EP]) {
-#pragma unroll
-    for (int p = 0; p < EP; ++p) {
-      const int r = (tid >> 4) + p * 4 * C::waves;
-      if (r < C::erows) es[r * 17 + (tid & 15)] = v[p];
+    for (int p = 0; p < C::eloads; ++p) {
+      const int r0 = 4 * (p * C::waves + wave), r = r0 + (lane >> 4);
+      const bool isx = p < C::xrows;
+      const uint32_t row = (uint32_t)(isx ? (int64_t)r * a.ldxe : (int64_t)(r - C::BT) * a.ldwe);
+      load_lds4_at(isx ? xer : wer, es0 + r0 * 64, row + 4u * ((lane & 15) ^ ((r >> 2) & 15)), (uint32_t)(kb0 & ~3));
     }
   };
 
@@ -247,10 +253,11 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
   // shifted to the step's byte apart from the read, which takes its time.
   auto read_exps = [&](int kb, int kb0, Exps& e) {
     const int d = (kb >> 2) - (kb0 >> 2);
+    auto at = [&](int r) { return (int)es[r * 16 + ((d ^ (r >> 2)) & 15)]; };
 #pragma unroll
-    for (int j = 0; j < C::EW; ++j) e.w[j] = (int)es[(C::BT + ((ncol0 + 32 * j) >> 7) - eb0) * 17 + d];
+    for (int j = 0; j < C::EW; ++j) e.w[j] = at(C::BT + ((ncol0 + 32 * j) >> 7) - eb0);
 #pragma unroll
-    for (int i = 0; i < C::FT; ++i) e.x[i] = (int)es[(xrow + 32 * i) * 17 + d];
+    for (int i = 0; i < C::FT; ++i) e.x[i] = at(xrow + 32 * i);
   };
   // Behind the group's last block the exponent is 0 (2^-127), not the byte that
   // happens to follow: 255 there would make the empty stage's zeros NaN.
@@ -290,15 +297,11 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
     }
   };
 
-  {
-    uint32_t ev[EP];
-    load_exps(k0, ev);
+  load_exps(k0);
 #pragma unroll
-    for (int s = 0; s < C::S; ++s)
+  for (int s = 0; s < C::S; ++s)
 #pragma unroll
-      for (int p = 0; p < C::loads; ++p) load(k0 + s, s, p);
-    store_exps(ev);
-  }
+    for (int p = 0; p < C::loads; ++p) load(k0 + s, s, p);
   wait_vm<(C::S - 1) * C::loads>();
   wait_lds();
   ring_barrier<C::waves>();
@@ -309,10 +312,8 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
   for (int i0 = 0; i0 < steps; i0 += kExpBlocks) {
     const int kb0 = k0 + i0;
     if (i0) {
-      uint32_t ev[EP];
-      load_exps(kb0, ev);
-      store_exps(ev);
-      wait_lds();
+      load_exps(kb0);
+      wait_vm<0>();
       ring_barrier<C::waves>();
     }
     Exps raw;

@@ -125,7 +125,7 @@ def test_q8_matmul_lds_loads_scalar_operands_and_no_scratch(q8_matmul_asm):
                 assert re.fullmatch(r"s\d+|vcc_(lo|hi)", m.group(1)), s
             if s.startswith("buffer_load"):
                 loads += 1
-                assert re.fullmatch(r"buffer_load_dwordx4 v\d+, s\[\d+:\d+\], (s\d+|vcc_(lo|hi)) offen lds", s), s
+                assert re.fullmatch(r"buffer_load_dword(x4)? v\d+, s\[\d+:\d+\], (s\d+|vcc_(lo|hi)) offen lds", s), s
         else:
             assert not re.search(r"\bm0\b", s), s
     assert loads > 0
