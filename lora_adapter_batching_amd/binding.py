@@ -517,6 +517,10 @@ def packed_backward_q8(x: Q8Rows, dy, u, adapters: Adapters, segments: Segments,
     lddx = _rows_arg("dx", dx, T, adapters.h_in, dev) if dx is not None else 0
     if u is None or u.get_device() != dev or u.dim() != 2 or u.shape[0] < T or u.stride(1) != 1 or u.element_size() != 4:
         raise ValueError(f"u must be a float32 [>= {T}, >= largest rank] matrix with unit column stride on {_dev_name(dev)}")
+    for name, t in (("adapters", adapters.A_ptrs), ("token_rows", segments.token_rows), ("dA_ptrs", dA_ptrs),
+                    ("dB_ptrs", dB_ptrs), ("ws", ws)):
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {_dev_name(dev)}")
     wp, wb = _ws(ws)
     _call_on(dev, stream, lib.lora_packed_backward_q8, x.addr, dy.data_ptr(), lddy, u.data_ptr(),
              u.stride(0), adapters.c, segments.c, _ptr(dx), lddx, _ptr(dA_ptrs), _ptr(dB_ptrs), int(flags), wp, wb)

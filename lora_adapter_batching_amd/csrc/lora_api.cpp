@@ -1087,6 +1087,9 @@ static int packed_backward_impl(const void* x, int64_t ldx, const void* dy, int6
       if (!u) return fail(LORA_INVALID_ARGUMENT, "u is NULL: the backward of a checkpoint needs the forward's u");
       if (x8->rows < segments->num_tokens)
         return fail(LORA_INVALID_ARGUMENT, "x has %d rows, the batch %d tokens", x8->rows, segments->num_tokens);
+      if (segments->token_rows && x8->ld_exps > x8->ld)
+        return fail(LORA_INVALID_ARGUMENT, "x: with token_rows, the exponent stride (%lld) must not exceed the row stride (%lld)",
+                    (long long)x8->ld_exps, (long long)x8->ld);
       if (segments->token_rows && (int64_t)(segments->num_tokens - 1) * x8->ld + x8->width > kGatherSpan)
         return fail(LORA_INVALID_ARGUMENT, "x: with token_rows, %d rows of stride %lld are above the %lld-byte gather limit",
                     segments->num_tokens, (long long)x8->ld, (long long)kGatherSpan);

@@ -372,7 +372,9 @@ int launched(const char* what) {
   return LORA_OK;
 }
 
-bool too_many(int64_t chunks) { return groups(chunks, 1) > 0x7fffffff / 4; }
+// A launch holds fewer than 2^32 threads.
+constexpr int64_t kMaxGroups = 0xffffffffll / kRowThreads;
+bool too_many(int64_t chunks) { return groups(chunks, many(chunks) ? 2 : 1) > kMaxGroups; }
 
 }  // namespace
 
@@ -426,6 +428,8 @@ extern "C" int lora_q8_quantize(const void* x, int64_t ldx, const lora_q8_t* out
   }
   if (out->rows == 0) return LORA_OK;
   if ((st = check_bf16_rows(x, ldx, out->width, "x"))) return st;
+  if (x == out->values || (out_t && (x == out_t->values || out->values == out_t->values)))
+    return set_error(LORA_INVALID_ARGUMENT, "a store starts at x or at the other store");
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (out->block_rows == kQ8Block) {
     WeightsArgs a{};
@@ -437,7 +441,7 @@ extern "C" int lora_q8_quantize(const void* x, int64_t ldx, const lora_q8_t* out
     }
     a.col_blocks = (int)q8_blocks(out->width);
     const int64_t n = q8_blocks(out->rows) * a.col_blocks;
-    if (n > 0x7fffffff) return set_error(LORA_UNSUPPORTED, "x of %d x %d is too large for one call", out->rows, out->width);
+    if (n > kMaxGroups) return set_error(LORA_UNSUPPORTED, "x of %d x %d is too large for one call", out->rows, out->width);
     hipLaunchKernelGGL(q8_weights_kernel, dim3((unsigned)n), dim3(256), 0, s, a);
     return launched("q8_weights");
   }
@@ -461,6 +465,7 @@ extern "C" int lora_q8_dequantize(const lora_q8_t* q, void* x, int64_t ldx, void
   if (st) return st;
   if (q->rows == 0) return LORA_OK;
   if ((st = check_bf16_rows(x, ldx, q->width, "x"))) return st;
+  if (x == q->values) return set_error(LORA_INVALID_ARGUMENT, "x starts at the store");
   RestoreArgs a{};
   a.values = q->values; a.ld = q->ld; a.exps = q->exps; a.ld_exps = q->ld_exps;
   a.x = static_cast<uint16_t*>(x); a.ldx = ldx;
@@ -495,6 +500,8 @@ static int gate_checks(const void* gate_up, int64_t ld, int32_t tokens, int32_t 
   if ((st = check_bf16_rows(gate_up, ld, 2 * (int64_t)width, "gate_up"))) return st;
   if (out && (st = check_bf16_rows(out, ldo, out_width, oname))) return st;
   if (out == gate_up) return set_error(LORA_INVALID_ARGUMENT, "%s starts at gate_up", oname);
+  if (outq && (outq->values == gate_up || outq->values == out))
+    return set_error(LORA_INVALID_ARGUMENT, "%s starts at gate_up or at %s", qname, oname);
   return LORA_OK;
 }
 
@@ -533,7 +540,8 @@ extern "C" int lora_swiglu_backward(const void* gate_up, int64_t ld, const void*
   int st = gate_checks(gate_up, ld, num_tokens, width, dgate_up, lddg, dgate_up_q, 2 * (int64_t)width, "dgate_up", "dgate_up_q");
   if (st || num_tokens == 0) return st;
   if ((st = check_bf16_rows(dh, lddh, width, "dh"))) return st;
-  if (dgate_up == dh) return set_error(LORA_INVALID_ARGUMENT, "dgate_up starts at dh");
+  if (dgate_up == dh || (dgate_up_q && dgate_up_q->values == dh))
+    return set_error(LORA_INVALID_ARGUMENT, "an output starts at dh");
   GateArgs a{};
   a.gate_up = static_cast<const uint16_t*>(gate_up); a.ld = ld;
   a.dh = static_cast<const uint16_t*>(dh); a.lddh = lddh;
@@ -544,7 +552,7 @@ extern "C" int lora_swiglu_backward(const void* gate_up, int64_t ld, const void*
   const bool split = q && (width % kQ8Block);
   a.cpr = split ? (uint32_t)q8_blocks(2 * (int64_t)width) * 16 : (uint32_t)width / 8;
   a.chunks = (int64_t)num_tokens * a.cpr;
-  if (too_many(a.chunks)) return set_error(LORA_UNSUPPORTED, "%d tokens of width %d are too many for one call", num_tokens, width);
+  if (groups(a.chunks, 1) > kMaxGroups) return set_error(LORA_UNSUPPORTED, "%d tokens of width %d are too many for one call", num_tokens, width);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const dim3 grid((unsigned)groups(a.chunks, 1)), blk(kRowThreads);
   const bool m = many(a.chunks);

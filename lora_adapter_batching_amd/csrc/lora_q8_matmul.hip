@@ -526,28 +526,31 @@ struct TileChoice {
   void (*launch)(MatArgs, bool, hipStream_t);
 };
 const TileChoice kTiles[] = {
-    {256, 256, 1, 256, 11.6f, 1.40f, launch_tile<Tile<256, 256, 2, 2, 2, 1, true>>},
-    {128, 128, 1, 512, 2.8f, 1.00f, launch_tile<Tile<128, 128, 2, 2, 2>>},
-    {128, 128, 1, 256, 6.9f, 0.34f, launch_tile<Tile<128, 128, 2, 2, 3>>},
-    {128, 160, 1, 256, 8.5f, 0.37f, launch_tile<Tile<128, 160, 4, 1, 3>>},
-    {128, 96, 1, 256, 7.0f, 0.26f, launch_tile<Tile<128, 96, 4, 1, 3>>},
-    {128, 64, 1, 256, 5.4f, 0.26f, launch_tile<Tile<128, 64, 2, 2, 3>>},
-    {32, 64, 4, 256, 4.0f, 0.56f, launch_tile<Tile<32, 64, 1, 2, 3, 4>>},
-    {32, 32, 4, 256, 4.2f, 0.39f, launch_tile<Tile<32, 32, 1, 1, 4, 4>>},
+    {256, 256, 1, 256, 10.6f, 1.40f, launch_tile<Tile<256, 256, 2, 2, 2, 1, true>>},
+    {128, 128, 1, 512, 2.4f, 1.00f, launch_tile<Tile<128, 128, 2, 2, 2>>},
+    {128, 128, 1, 256, 6.2f, 0.34f, launch_tile<Tile<128, 128, 2, 2, 3>>},
+    {128, 160, 1, 256, 7.6f, 0.37f, launch_tile<Tile<128, 160, 4, 1, 3>>},
+    {128, 96, 1, 256, 6.3f, 0.26f, launch_tile<Tile<128, 96, 4, 1, 3>>},
+    {128, 64, 1, 256, 4.9f, 0.26f, launch_tile<Tile<128, 64, 2, 2, 3>>},
+    {32, 64, 4, 256, 3.4f, 0.56f, launch_tile<Tile<32, 64, 1, 2, 3, 4>>},
+    {32, 32, 4, 256, 3.1f, 0.39f, launch_tile<Tile<32, 32, 1, 1, 4, 4>>},
 };
+
+constexpr int64_t kMaxTiles = 0xffffffffll / 512;
 
 void launch_matmul(const MatArgs& a, bool add, hipStream_t s) {
   // One matrix fragment of tokens: the weights' bytes are all that counts (one
   // token 2560 -> 2560: 4.0 us against 6.2 with 32 x 32 tiles, 2560 -> 19456: 11
   // against 13 with 128 x 96; 16 tokens 4.9 against 6.2 and 15 against 13, 9728 ->
   // 2560: 12 either way).
-  if (a.T <= kFewTokens) return launch_few(a, add, s);
+  // (A launch holds fewer than 2^32 threads, 512 of them per workgroup.)
+  if (a.T <= kFewTokens && a.N <= 1 << 26) return launch_few(a, add, s);
   const TileChoice* best = &kTiles[0];  // (its grid is checked by the caller)
   double least = 0.;
   for (const TileChoice& c : kTiles) {
     const int64_t tiles = ((int64_t)a.T + c.bt - 1) / c.bt * (((int64_t)a.N + c.bn - 1) / c.bn);
     const double t = (double)((tiles + c.slots - 1) / c.slots) * (c.fixed + (double)c.step * ((a.nkb + c.ks - 1) / c.ks));
-    if (&c == best || (t < least && tiles <= 0x7fffffff)) best = &c, least = t;
+    if (&c == &kTiles[0] || (t < least && tiles <= kMaxTiles)) best = &c, least = t;
   }
   best->launch(a, add, s);
 }
@@ -574,7 +577,7 @@ extern "C" int lora_q8_matmul(const lora_q8_t* x, const lora_q8_t* w, void* y, i
   const int64_t most = 0x7fffff00 / 256;
   if (x->ld > most || w->ld > most || x->ld_exps > most || w->ld_exps > most)
     return set_error(LORA_UNSUPPORTED, "row strides above %lld bytes are not supported", (long long)most);
-  if (((int64_t)x->rows + 255) / 256 * (((int64_t)w->rows + 255) / 256) > 0x7fffffff || x->rows > 0x7fffff00 || w->rows > 0x7fffff00)
+  if (((int64_t)x->rows + 255) / 256 * (((int64_t)w->rows + 255) / 256) > kMaxTiles || x->rows > 0x7fffff00 || w->rows > 0x7fffff00)
     return set_error(LORA_UNSUPPORTED, "y of %d x %d is too large for one call", x->rows, w->rows);
   MatArgs a{};
   a.x = x->values; a.ldx = x->ld; a.xe = x->exps; a.ldxe = x->ld_exps;

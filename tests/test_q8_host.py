@@ -78,7 +78,12 @@ def test_quantize_refusals():
         st, msg = status(lib.lora_q8_quantize, args[0], args[1], ctypes.byref(args[2]) if args[2] else None,
                          ctypes.byref(args[3]) if args[3] else None, None)
         assert st == B.LORA_INVALID_ARGUMENT and word in msg, (args, msg)
-    for x, ld, word in [(0, 256, "NULL"), (P + 2, 256, "aligned"), (P, 128, "below its width")]:
+    D = 1 << 41
+    wq, wt = q8(rows=8, block_rows=128), q8(rows=256, width=8, ld=128, block_rows=128)
+    for x, a, b in [(P, o, None), (P, wq, q8(rows=256, width=8, ld=128, block_rows=128, values=D)), (D, wq, wt)]:
+        st, msg = status(lib.lora_q8_quantize, x, 256, ctypes.byref(a), ctypes.byref(b) if b else None, None)
+        assert st == B.LORA_INVALID_ARGUMENT and "starts at" in msg, msg
+    for x, ld, word in [(P, 256, "starts at"), (0, 256, "NULL"), (P + 2, 256, "aligned"), (P, 128, "below its width")]:
         st, msg = status(lib.lora_q8_dequantize, ctypes.byref(o), x, ld, None)
         assert st == B.LORA_INVALID_ARGUMENT and word in msg, msg
 
@@ -112,14 +117,16 @@ def test_swiglu_refusals():
                        ((0, 256, 4, 128, D, 128, None), "NULL"), ((P + 2, 256, 4, 128, D, 128, None), "aligned"),
                        ((P, 248, 4, 128, D, 128, None), "below its width"), ((P, 256, 4, 128, D, 120, None), "below its width"),
                        ((P, 256, 5, 128, None, 0, by(hq)), "expected 5"), ((P, 256, 4, 136, None, 0, by(hq)), "expected 4"),
-                       ((P, 256, 4, 128, P, 256, None), "starts at")]:
+                       ((P, 256, 4, 128, P, 256, None), "starts at"), ((P, 256, 4, 128, None, 0, by(hq)), "starts at"),
+                       ((D, 256, 4, 128, P, 128, by(hq)), "starts at")]:
         st, msg = status(lib.lora_swiglu, *args, None)
         assert st == B.LORA_INVALID_ARGUMENT and word in msg, (args, msg)
     for args, word in [((P, 256, D, 128, -1, 128, D * 2, 256, None), "num_tokens"), ((P, 256, 0, 128, 4, 128, D * 2, 256, None), "NULL"),
                        ((P, 256, D, 120, 4, 128, D * 2, 256, None), "below its width"), ((P, 256, D, 128, 4, 128, None, 0, None), "both NULL"),
                        ((P, 256, D, 128, 4, 128, D * 2, 128, None), "below its width"),
                        ((P, 256, D, 128, 4, 128, None, 0, by(hq)), "expected 4 x 256"), ((P, 256, D, 128, 5, 128, None, 0, by(gq)), "expected 5"),
-                       ((P, 256, D, 128, 4, 128, P, 256, None), "starts at"), ((P, 256, D, 128, 4, 128, D, 256, None), "starts at")]:
+                       ((P, 256, D, 128, 4, 128, P, 256, None), "starts at"), ((P, 256, D, 128, 4, 128, D, 256, None), "starts at"),
+                       ((D, 256, P, 128, 4, 128, None, 0, by(gq)), "starts at"), ((P, 256, D, 128, 4, 128, None, 0, by(gq)), "starts at")]:
         st, msg = status(lib.lora_swiglu_backward, *args, None)
         assert st == B.LORA_INVALID_ARGUMENT and word in msg, (args, msg)
 
@@ -149,11 +156,26 @@ def test_backward_refusals():
     call(1, "values/exps", _backward_args(x=q8(values=0)))
     call(2, "strides", _backward_args(x=q8(ld=1 << 26)))
     call(1, "gather limit", _backward_args(x=q8(rows=200, ld=1 << 24), T=200, rows_dev=P))
+    call(1, "exponent stride", _backward_args(x=q8(lde=512), rows_dev=P))
     call(1, "flags", _backward_args(), flags=2)
     call(3, "workspace", _backward_args(), wb=16)
     keep, a = _backward_args()
     st, msg = status(lib.lora_packed_backward_q8, None, *a[1:], 0, P, 1 << 40, None)
     assert st == 1 and "x is NULL" in msg
+
+
+def test_more_than_one_launch_holds_is_refused():
+    """Grids of 2^32 threads and more (stand-in addresses: nothing is launched)."""
+    lib = L.load()
+    by, big, D = ctypes.byref, 0x7fffff00, 1 << 41
+    for fn, *args in [(lib.lora_q8_quantize, D, 4096, by(q8(rows=big, width=4096, ld=4096, lde=32)), None),
+                      (lib.lora_q8_quantize, D, 1 << 20, by(q8(rows=big, width=1 << 20, ld=1 << 20, lde=1 << 13, block_rows=128)), None),
+                      (lib.lora_q8_dequantize, by(q8(rows=big, width=4096, ld=4096, lde=32)), D, 4096),
+                      (lib.lora_q8_matmul, by(q8(rows=big)), by(q8(rows=big, block_rows=128)), D, big, 0),
+                      (lib.lora_swiglu, D, 8192, big, 4096, 2 * D, 4096, None),
+                      (lib.lora_swiglu_backward, D, 8192, 4 * D, 4096, big, 4096, 2 * D, 8192, None)]:
+        st, msg = status(fn, *args, None)
+        assert st == B.LORA_UNSUPPORTED, (fn, st, msg)
 
 
 def test_no_rows_is_no_work():
