@@ -465,6 +465,11 @@ def _q8_arg(name: str, q: _Q8, dev: int) -> int:
     return q.addr
 
 
+def _largest_rank(adapters: Adapters, segments: Segments) -> int:
+    used = segments.seg_adapter[(segments.seg_adapter >= 0) & (segments.seg_adapter < len(adapters.ranks))]
+    return int(adapters.ranks[used].max(initial=0))
+
+
 def _dev_name(dev: int) -> str:
     return f"cuda:{dev}" if dev >= 0 else "cpu"
 
@@ -515,7 +520,9 @@ def packed_backward_q8(x: Q8Rows, dy, u, adapters: Adapters, segments: Segments,
     lib, T, dev = _lib or load(), segments.num_tokens, x.dev
     lddy = _rows_arg("dy", dy, T, adapters.h_out, dev)
     lddx = _rows_arg("dx", dx, T, adapters.h_in, dev) if dx is not None else 0
-    if u is None or u.get_device() != dev or u.dim() != 2 or u.shape[0] < T or u.stride(1) != 1 or u.element_size() != 4:
+    # (rows that follow each other are as wide as their stride, which the call checks)
+    if (u is None or u.get_device() != dev or u.dtype is not _torch.float32 or u.dim() != 2 or u.shape[0] < T
+            or u.stride(1) != 1 or u.shape[1] != u.stride(0) and u.shape[1] < _largest_rank(adapters, segments)):
         raise ValueError(f"u must be a float32 [>= {T}, >= largest rank] matrix with unit column stride on {_dev_name(dev)}")
     for name, t in (("adapters", adapters.A_ptrs), ("token_rows", segments.token_rows), ("dA_ptrs", dA_ptrs),
                     ("dB_ptrs", dB_ptrs), ("ws", ws)):

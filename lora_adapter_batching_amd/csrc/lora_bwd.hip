@@ -147,7 +147,6 @@ struct WgShareX {
   float e[2][2][32];             // [buffer][block][token]
 };
 
-
 __device__ __forceinline__ void wg_advance(const WgradPlan& P, int seg_end, WgCursor& c) {
   c.t0 += 32;
   while (c.t0 >= c.tend && c.seg < seg_end) {
@@ -515,7 +514,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradPlan P) {
   if constexpr (X8) {
     // one read per 64-byte line of the plan, all at once: the dependent reads
     // below then find it in L2 instead of going to memory one by one (a step
-    // of 24 rows: 8.2 -> 6.8 us; one of 16384 rows: 187 us either way)
+    // of 24 rows: 8.2 -> 6.8 us; one of 65536 rows: 187 us either way)
     const uint32_t* line = (const uint32_t*)(const void*)__builtin_amdgcn_kernarg_segment_ptr();
     uint32_t word = 0;
     if (threadIdx.x < sizeof(WgradPlan) / 64) word = line[16 * threadIdx.x];

@@ -69,11 +69,13 @@ __device__ __forceinline__ void load_lds16_at(i32x4 rsrc, uint32_t lds_addr, uin
                : "memory");
   (void)m0_out;
 }
-__device__ __forceinline__ void load_lds4_at(i32x4 rsrc, uint32_t lds_addr, uint32_t voff, uint32_t soff) {
+// (Dwords are the exponents'. Their row may end inside a load, so the whole
+// position is in the vector offset, which the descriptor checks.)
+__device__ __forceinline__ void load_lds4_at(i32x4 rsrc, uint32_t lds_addr, uint32_t voff) {
   int m0_out;
   asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dword %2, %3, %4 offen lds"
                : "={m0}"(m0_out)
-               : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
+               : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(0)
                : "memory");
   (void)m0_out;
 }
@@ -226,7 +228,7 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
       const int r0 = 4 * (p * C::waves + wave), r = r0 + (lane >> 4);
       const bool isx = p < C::xrows;
       const uint32_t row = (uint32_t)(isx ? (int64_t)r * a.ldxe : (int64_t)(r - C::BT) * a.ldwe);
-      load_lds4_at(isx ? xer : wer, es0 + r0 * 64, row + 4u * ((lane & 15) ^ ((r >> 2) & 15)), (uint32_t)(kb0 & ~3));
+      load_lds4_at(isx ? xer : wer, es0 + r0 * 64, row + 4u * ((lane & 15) ^ ((r >> 2) & 15)) + (uint32_t)(kb0 & ~3));
     }
   };
 

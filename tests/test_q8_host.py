@@ -247,3 +247,21 @@ def test_reference_swiglu_gradient_against_differences():
             d[i, j] = step
             num = (np.sum(dh * R.swiglu(x + d)[3]) - np.sum(dh * R.swiglu(x - d)[3])) / (2 * step)
             assert abs(num - g[i, j]) < 1e-7 * (1 + abs(num)), (i, j)  # step^2 and 1e-16 / step
+
+
+def test_binding_refuses_a_u_that_is_narrower_than_its_ranks():
+    """A column slice has the stride of the matrix it is cut from, so only its
+    width says that it does not hold the ranks."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    ad = L.Adapters([bf(16, 256), bf(8, 256)], [bf(64, 16), bf(64, 8)], [16, 8], [1.0, 1.0], 256, 64, device="cpu")
+    q, dy, tab = L.new_q8_rows(4, 256, "cpu"), bf(4, 64), torch.zeros(2, dtype=torch.int64)
+    full = torch.zeros((4, 64))
+    wide, narrow = L.Segments([0, 2, 4], [0, -1]), L.Segments([0, 4], [1])
+    call = lambda u, seg: L.packed_backward_q8(q, dy, u, ad, seg, None, tab, tab)  # noqa: E731
+    for u, seg in [(full[:, :8], wide), (full[:, 56:], wide), (full[:, :4], narrow), (full[:3], narrow), (full.double(), narrow),
+                   (torch.zeros((4, 64), dtype=torch.int32), narrow), (full.t(), narrow), (None, narrow)]:
+        with pytest.raises(ValueError, match="u must be"):
+            call(u, seg)
+    for u, seg in [(full, wide), (full[:, :16], wide), (full[:, :8], narrow)]:
+        with pytest.raises(ValueError, match="device tensors"):
+            call(u, seg)
