@@ -128,7 +128,11 @@ struct WgRegs {
 // leave about 3e-6). The parts are made once per step, by the thread that loads
 // a pair of tokens' values, and go through LDS as MFMA operands; made in every
 // wave from fp32 in LDS, they took more time than the step's loads (dA and dB
-// of 65536 tokens, 3584 -> 3584, 32 adapters: 206 us).
+// of 65536 tokens, 3584 -> 3584, 32 adapters: 206 us, now 188). The matrix
+// unit is then busy for 19% of the time and memory moves 0.95 GB at 5.0 TB/s,
+// a large copy's rate. 0.73 GB are needed; the rest is u and du, which every
+// XCD reads. With whole jobs on one XCD 0.76 GB are left and the launch takes
+// 186 us, with half the LDS and three workgroups a CU it is 10 us slower.
 //
 // Z of dA is then e4m3: the same rows and columns as bytes, and one exponent
 // byte per token and 128 columns. An item's columns (256 for QN = 4, 128 for

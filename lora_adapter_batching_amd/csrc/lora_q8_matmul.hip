@@ -133,7 +133,7 @@ __device__ __forceinline__ void tile_of(const MatArgs& a, int b, int grid, int& 
 //    same time, and 4 MB of y an XCD would push the rows of the next tiles out of
 //    its L2 (395 us without). Smaller tiles keep plain stores: their y
 //    is small and the next operator reads it.
-// Now 361-371 us, 2.6 PFLOP/s (the library's fp8 product without block scales:
+// Now 355-371 us, 2.6-2.7 PFLOP/s (the library's fp8 product without block scales:
 // 384). The steps run at 3.0; the rest is each tile's start and end (6 us of 52).
 // ---------------------------------------------------------------------------
 template <int BT_, int BN_, int WT_, int WN_, int S_, int KS_ = 1, bool STREAM_ = false>
