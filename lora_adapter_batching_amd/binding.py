@@ -480,6 +480,8 @@ def _call_on(dev: int, stream, fn, *args):
     few microseconds of GPU work, so the host's share is kept small.)"""
     if dev < 0:
         raise ValueError("device tensors are needed, got cpu")
+    if stream is not None and getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors are on cuda:{dev}")
     cuda = _torch._C
     if dev != cuda._cuda_getDevice():
         with _torch.cuda.device(dev):

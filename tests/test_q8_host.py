@@ -265,3 +265,14 @@ def test_binding_refuses_a_u_that_is_narrower_than_its_ranks():
     for u, seg in [(full, wide), (full[:, :16], wide), (full[:, :8], narrow)]:
         with pytest.raises(ValueError, match="device tensors"):
             call(u, seg)
+
+
+def test_binding_refuses_another_devices_stream():
+    class Stream:
+        device_index, cuda_stream = 1, 0
+
+    def launch(*_):
+        raise AssertionError("launched")
+
+    with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
+        L.binding._call_on(0, Stream(), launch)
