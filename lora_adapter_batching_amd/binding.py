@@ -453,6 +453,8 @@ def _rows_arg(name: str, t, rows: int, width: int, dev: int) -> int:
         shape = t.shape
         if len(shape) == 2 and shape[0] >= rows and shape[1] == width:
             stride, step = t.stride()
+            if shape[0] <= 1 and (step == 1 or shape[0] == 0):
+                return width  # (a row that no other follows may have any stride)
             if step == 1:
                 return stride
     raise ValueError(f"{name} must be a bfloat16 [>= {rows}, {width}] matrix with unit column stride on "
@@ -522,17 +524,20 @@ def packed_backward_q8(x: Q8Rows, dy, u, adapters: Adapters, segments: Segments,
     lib, T, dev = _lib or load(), segments.num_tokens, x.dev
     lddy = _rows_arg("dy", dy, T, adapters.h_out, dev)
     lddx = _rows_arg("dx", dx, T, adapters.h_in, dev) if dx is not None else 0
+    ldu = 0
+    if u is not None and u.dim() == 2:
+        ldu = u.stride(0) if u.shape[0] > 1 else u.shape[1]
     # (rows that follow each other are as wide as their stride, which the call checks)
     if (u is None or u.get_device() != dev or u.dtype is not _torch.float32 or u.dim() != 2 or u.shape[0] < T
-            or u.stride(1) != 1 or u.shape[1] != u.stride(0) and u.shape[1] < _largest_rank(adapters, segments)):
+            or u.shape[0] > 0 and u.stride(1) != 1 or u.shape[1] != ldu and u.shape[1] < _largest_rank(adapters, segments)):
         raise ValueError(f"u must be a float32 [>= {T}, >= largest rank] matrix with unit column stride on {_dev_name(dev)}")
     for name, t in (("adapters", adapters.A_ptrs), ("token_rows", segments.token_rows), ("dA_ptrs", dA_ptrs),
                     ("dB_ptrs", dB_ptrs), ("ws", ws)):
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, expected {_dev_name(dev)}")
     wp, wb = _ws(ws)
-    _call_on(dev, stream, lib.lora_packed_backward_q8, x.addr, dy.data_ptr(), lddy, u.data_ptr(),
-             u.stride(0), adapters.c, segments.c, _ptr(dx), lddx, _ptr(dA_ptrs), _ptr(dB_ptrs), int(flags), wp, wb)
+    _call_on(dev, stream, lib.lora_packed_backward_q8, x.addr, dy.data_ptr(), lddy, u.data_ptr(), ldu,
+             adapters.c, segments.c, _ptr(dx), lddx, _ptr(dA_ptrs), _ptr(dB_ptrs), int(flags), wp, wb)
 
 
 def swiglu(gate_up, h=None, hq: Optional[Q8Rows] = None, stream=None):

@@ -493,6 +493,28 @@ def test_packed_backward_q8_gather_outside_rows_read_as_zero():
     assert torch.equal(dx[[3, 17]], p.dx0[[3, 17]])
 
 
+@pytest.mark.parametrize("segs", [([0], []), ([0, 0, 0], [1, 0])])
+def test_packed_backward_q8_without_tokens(segs):
+    """No token at all: gradients are zeroed, or kept when they are added to."""
+    rng = np.random.default_rng(17)
+    p = Packed(rng, 0, 136, 264, [8, 64], *segs)
+    dx = p.dx0.clone()
+    p.call(dx, L.GRAD_ACCUMULATE)
+    torch.cuda.synchronize()
+    assert all(torch.all(t == 3) for t in p.dA + p.dB)
+    p.call(dx)
+    torch.cuda.synchronize()
+    assert not any(t.any() for t in p.dA + p.dB)
+
+
+def test_packed_backward_q8_one_token_of_a_strided_batch():
+    """One token that names the sixth row of dy and dx, which lie in wider matrices."""
+    p = Packed(np.random.default_rng(18), 1, 136, 264, [16], [0, 1], [0], perm=[5], pad_rows=7)
+    p.dy, dx = strided(p.dy)[1], strided(p.dx0)[1]
+    p.call(dx)
+    p.check(dx)
+
+
 def test_packed_backward_q8_equals_packed_backward_on_restored_rows():
     """The same batch through lora_packed_backward with x restored to bf16 (exact): dx and dB see the same operands."""
     p = BACKWARD["two_segments_and_none"](np.random.default_rng(4))

@@ -276,3 +276,14 @@ def test_binding_refuses_another_devices_stream():
 
     with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
         L.binding._call_on(0, Stream(), launch)
+
+
+def test_binding_takes_rows_that_no_other_follows_with_any_stride():
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    one = bf(256, 1).t()                                         # [1, 256] with strides (1, 1)
+    none = bf(256, 4).t()[:0]                                    # [0, 256] with strides (1, 4)
+    assert L.binding._rows_arg("x", one, 1, 256, -1) == 256 and L.binding._rows_arg("x", none, 0, 256, -1) == 256
+    for rows in (0, 1, 4):                                       # (a call of one token may name any of the rows)
+        assert L.binding._rows_arg("x", bf(4, 264)[:, :256], rows, 256, -1) == 264
+    with pytest.raises(ValueError):
+        L.binding._rows_arg("x", bf(256, 2).t(), 1, 256, -1)     # a row that is itself strided
