@@ -58,12 +58,17 @@ __device__ __forceinline__ i32x4 mk_rsrc_words(const void* base, int64_t bytes) 
 // statement, so the compiler keeps no value of its own in it across the load.
 // The descriptor words pass through readfirstlane so that they are SGPR
 // values even where the compiler has kept a copy of them in VGPRs.
+// The hardware does not interlock two of the values that such a load reads:
+// M0 has to be one wait state old, and a scalar register that a vector
+// instruction wrote (readfirstlane just in front) five. The compiler inserts
+// these waits around its own instructions only, not inside inline assembly, so
+// the statement holds them: s_mov is one, s_nop 3 four.
 __device__ __forceinline__ void load_lds16(i32x4 rsrc, uint32_t lds_addr, uint32_t voff) {
   int m0_out;
   i32x4 r;
 #pragma unroll
   for (int q = 0; q < 4; ++q) r[q] = __builtin_amdgcn_readfirstlane(rsrc[q]);
-  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
                : "={m0}"(m0_out)
                : "s"(lds_addr), "v"(voff), "s"(r)
                : "memory");
@@ -75,7 +80,7 @@ __device__ __forceinline__ void load_lds16_stream(i32x4 rsrc, uint32_t lds_addr,
   i32x4 r;
 #pragma unroll
   for (int q = 0; q < 4; ++q) r[q] = __builtin_amdgcn_readfirstlane(rsrc[q]);
-  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen nt lds"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_dwordx4 %2, %3, 0 offen nt lds"
                : "={m0}"(m0_out)
                : "s"(lds_addr), "v"(voff), "s"(r)
                : "memory");

@@ -139,3 +139,86 @@ def test_q8_matmul_lds_loads_scalar_operands_and_no_scratch(q8_matmul_asm):
         for b in loops:
             inner = re.split(r"v_mfma", b)[1:-1]
             assert not any(re.search(r"global_(load|store)|buffer_store|flat_", p) for p in inner), k.split(":")[0]
+
+
+# ---------------------------------------------------------------------------
+# Wait states in front of the LDS-destination loads
+# ---------------------------------------------------------------------------
+_SGPR = re.compile(r"\bs\[(\d+):(\d+)\]|\bs(\d+)\b|\b(vcc|m0)(?:_lo|_hi)?\b")
+
+
+def _scalar_registers(text):
+    regs = set()
+    for lo, hi, one, name in _SGPR.findall(text):
+        regs |= {name} if name else {f"s{i}" for i in (range(int(lo), int(hi) + 1) if lo else [int(one)])}
+    return regs
+
+
+def _early_lds_loads(text):
+    """(loads, those that read M0 less than one wait state after its write or a
+    scalar register less than five after a vector instruction's write of it).
+    Every instruction is one wait state, s_nop n is n + 1; all paths into a
+    load are followed, through branches too."""
+    ins, labels = [], {}                       # (opcode, operands) in order; label -> place
+    for line in text.splitlines():
+        s = re.split(r";|//", line)[0].strip()
+        if re.fullmatch(r"[.\w$]+:", s):
+            labels[s[:-1]] = len(ins)
+        elif s and not s.startswith("."):
+            op, _, rest = s.partition(" ")
+            ins.append((op, rest))
+    from_branch = {}
+    for i, (op, rest) in enumerate(ins):
+        if op.startswith(("s_cbranch", "s_branch")):
+            from_branch.setdefault(labels[rest.strip()], []).append(i)
+
+    def before(i):
+        prev = from_branch.get(i, [])
+        return prev + ([i - 1] if i and ins[i - 1][0] not in ("s_branch", "s_endpgm", "s_setpc_b64") else [])
+
+    loads, early = 0, []
+    for i, (op, rest) in enumerate(ins):
+        if not op.startswith("buffer_load") or not re.search(r"\blds\b", rest):
+            continue
+        loads += 1
+        reads, todo = _scalar_registers(rest), [(j, 0) for j in before(i)]
+        while todo:
+            j, waited = todo.pop()
+            o, r = ins[j]
+            dst = r.split(",")[0]
+            if o.startswith("v_"):             # carries are the second destination
+                dst += "," + r.split(",")[1] if re.search(r"_co_|div_scale", o) and "," in r else ""
+                if _scalar_registers(dst) & reads:
+                    early.append((i, o, r, rest, waited))
+            elif waited < 1 and "m0" in _scalar_registers(dst) and not o.startswith(("s_cmp", "buffer_")):
+                early.append((i, o, r, rest, waited))
+            waited += int(r, 0) + 1 if o == "s_nop" else 1
+            if waited < 5:
+                todo += [(k, waited) for k in before(j)]
+    return loads, early
+
+
+def test_lds_loads_wait_for_their_scalar_registers(fwd_asm, q8_matmul_asm):
+    """M0 is one wait state old and every scalar register that a vector
+    instruction wrote five when an LDS-destination load reads it."""
+    for text in (fwd_asm, q8_matmul_asm):
+        loads, early = _early_lds_loads(text)
+        assert loads > 0
+        assert not early, (len(early), early[:3])
+
+
+def test_wait_state_count_follows_branches_and_nops():
+    """The counting itself, on short listings of each kind."""
+    load = "buffer_load_dwordx4 v1, s[4:7], s9 offen lds"
+    first = "v_readfirstlane_b32 s6, v0"
+    for lines, n in [(["s_mov_b32 m0, s2", load], 1), (["s_mov_b32 m0, s2", "s_nop 0", load], 0),
+                     ([first, "s_mov_b32 m0, s2", "s_nop 3", load], 0), ([first, "s_mov_b32 m0, s2", "s_nop 2", load], 1),
+                     (["v_readfirstlane_b32 s9, v0", "s_mov_b32 m0, s2", "s_nop 0", load], 1),
+                     (["v_readfirstlane_b32 s8, v0", "s_mov_b32 m0, s2", "s_nop 0", load], 0),
+                     ([first, "s_cbranch_scc1 .L1", "s_nop 7", ".L1:", "s_mov_b32 m0, s2", "s_nop 1", load], 1),
+                     ([first, "s_branch .L1", ".L2:", "s_endpgm", ".L1:", "s_mov_b32 m0, s2", "s_nop 3", load], 0),
+                     ([".L1:", "s_mov_b32 m0, s2", "s_nop 0", load, first, "s_cbranch_scc1 .L1"], 1),
+                     (["v_cmp_eq_u32_e64 s[6:7], v0, v1", "s_mov_b32 m0, s2", "s_nop 0", load], 1),
+                     (["v_add_co_u32_e64 v0, s[6:7], v0, v1", "s_mov_b32 m0, s2", "s_nop 0", load], 1)]:
+        loads, early = _early_lds_loads("\n".join(lines))
+        assert loads == 1 and len(early) == n, lines
