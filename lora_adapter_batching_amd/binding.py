@@ -399,24 +399,31 @@ class _Q8:
 
     def __init__(self, values, exps, width: int, rows: Optional[int] = None):
         import torch
-        if values.dtype not in (torch.uint8, torch.float8_e4m3fn) or values.dim() != 2 or values.stride(1) != 1:
+        if (values.dtype not in (torch.uint8, torch.float8_e4m3fn) or values.dim() != 2
+                or values.shape[0] > 0 and values.stride(1) != 1):
             raise ValueError("values must be a 2-D uint8 or float8_e4m3fn tensor with unit column stride")
-        if exps.dtype != torch.uint8 or exps.dim() != 2 or exps.stride(1) != 1:
+        if exps.dtype != torch.uint8 or exps.dim() != 2 or exps.shape[0] > 0 and exps.stride(1) != 1:
             raise ValueError("exps must be a 2-D uint8 tensor with unit column stride")
         self.rows = int(values.shape[0] if rows is None else rows)
         self.width = int(width)
         blocks, erows = -(-self.width // 128), -(-self.rows // self.block_rows)
+        whole = -(-blocks // 4) * 4  # whole dwords of exponents: the products read four blocks at a time
         if self.rows < 0 or self.rows > values.shape[0] or values.shape[1] < 128 * blocks:
             raise ValueError(f"values of shape {tuple(values.shape)} do not hold {self.rows} rows of {128 * blocks} bytes")
-        # whole dwords of exponents: the products read four blocks at a time
-        if exps.shape[0] < erows or exps.stride(0) < -(-blocks // 4) * 4 or exps.shape[1] < blocks:
+        ld, lde = values.stride(0), exps.stride(0)
+        # (a row that no other follows may have any stride)
+        if self.rows <= 1:
+            ld = 128 * blocks
+        if erows == 0 or erows == 1 and max(exps.shape[1], lde) >= whole:
+            lde = whole
+        if exps.shape[0] < erows or lde < whole or exps.shape[1] < blocks:
             raise ValueError(f"exps of shape {tuple(exps.shape)} do not hold {erows} rows of {blocks} blocks "
                              "with a stride that is a multiple of 4")
         if values.device != exps.device:
             raise ValueError(f"values are on {values.device}, exps on {exps.device}")
         self.values, self.exps = values, exps
         self.dev = values.get_device()
-        self._c = CQ8(_ptr(values), values.stride(0), _ptr(exps), exps.stride(0), self.rows, self.width,
+        self._c = CQ8(_ptr(values), ld, _ptr(exps), lde, self.rows, self.width,
                       self.block_rows)
         self.addr = ctypes.addressof(self._c)
 

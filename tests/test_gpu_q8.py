@@ -740,3 +740,18 @@ def test_oracle_packed_batch_from_a_checkpoint():
         for got, want in ((dA[a], dA_ref[a]), (dB[a], dB_ref[a])):
             want = np.asarray(want).reshape(got.shape)
             held(got.cpu().numpy(), want, 2.0 ** -14 * max(np.abs(want).max(), 1e-30))
+
+
+def test_single_stored_row_of_any_stride():
+    """One token whose bytes and exponents are columns of wider tensors: stored, restored and multiplied like a row of its own."""
+    rng = np.random.default_rng(23)
+    x, w = rows(rng, 1, 600), stored(rows(rng, 72, 600, 0.1), weights=True)
+    byte = lambda n, fill: torch.full((n, 1), fill, dtype=torch.uint8, device="cuda").t()  # noqa: E731
+    q = L.Q8Rows(byte(R.padded(600), 0xAB), byte(8, 255), 600)
+    L.q8_quantize(x, q)
+    check_store(q, to_f64(x))
+    back, y = torch.empty_like(x), torch.empty((1, 72), dtype=torch.bfloat16, device="cuda")
+    L.q8_dequantize(q, back)
+    assert np.array_equal(to_f64(back), R.read_store(q))
+    L.q8_matmul(q, w, y)
+    check_matmul(q, w, y)

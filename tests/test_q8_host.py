@@ -287,3 +287,24 @@ def test_binding_takes_rows_that_no_other_follows_with_any_stride():
         assert L.binding._rows_arg("x", bf(4, 264)[:, :256], rows, 256, -1) == 264
     with pytest.raises(ValueError):
         L.binding._rows_arg("x", bf(256, 2).t(), 1, 256, -1)     # a row that is itself strided
+
+
+def test_binding_takes_a_single_stored_row_of_any_stride():
+    """A store whose row no other follows, as a slice of a tensor of another
+    layout: the strides it hands over are those of a store of its own."""
+    wide = lambda n: torch.zeros((n, 1), dtype=torch.uint8).t()                   # noqa: E731  [1, n] with strides (1, 1)
+    exps = torch.zeros((3, 6), dtype=torch.uint8)[1:2, :4]                        # a stride of 6
+    for q, want in [(L.Q8Rows(wide(256), wide(4), 256), (256, 4)), (L.Q8Rows(wide(640), wide(8), 600), (640, 8)),
+                    (L.Q8Rows(torch.zeros((1, 256), dtype=torch.uint8), exps, 256), (256, 4)),
+                    (L.Q8Rows(torch.zeros((4, 264), dtype=torch.uint8)[:, :256], exps, 256, rows=1), (256, 4)),
+                    (L.Q8Weights(torch.zeros((128, 256), dtype=torch.uint8), exps, 256), (256, 4)),
+                    (L.Q8Rows(torch.zeros((256, 4), dtype=torch.uint8).t()[:0], torch.zeros((4, 2), dtype=torch.uint8).t()[:0], 256), (256, 4))]:
+        assert (q._c.ld, q._c.ld_exps) == want
+        # (the store's own checks pass: what is refused is the matrix beside it)
+        st, msg = status(L.load().lora_q8_dequantize, ctypes.byref(B.CQ8(P, q._c.ld, P, q._c.ld_exps, 1, q.width, q.block_rows)), 0, 0, None)
+        assert st == B.LORA_INVALID_ARGUMENT and "x is NULL" in msg, msg
+    for v, e in [(wide(256), wide(2)),                                           # two bytes of exponents: not a whole dword
+                 (torch.zeros((2, 256), dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.uint8).t()),  # two rows, strides (1, 2)
+                 (torch.zeros((256, 2), dtype=torch.uint8).t(), torch.zeros((2, 4), dtype=torch.uint8))]:
+        with pytest.raises(ValueError):
+            L.Q8Rows(v, e, 256)
