@@ -60,18 +60,21 @@ __device__ __forceinline__ f32x4 mfma8_16(i32x8 a, i32x8 b, f32x4 c, int ea, int
 
 // LDS-destination loads whose k position is a scalar offset. The descriptor
 // ends with the last valid row; rows behind it have vector offsets past its
-// end (with or without the scalar offset counted) and write zeros. (The waits
-// between the scalar registers' writes and the load: load_lds16.)
+// end (with or without the scalar offset counted) and write zeros.
+// M0 gets its wait state here (load_lds16 has the rule); the descriptor and the
+// offset come from scalar instructions in the steps (all five waits: 374 instead
+// of 371 us for 8192 tokens 4096 -> 14336), which the instruction-level tests check.
 __device__ __forceinline__ void load_lds16_at(i32x4 rsrc, uint32_t lds_addr, uint32_t voff, uint32_t soff) {
   int m0_out;
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds"
                : "={m0}"(m0_out)
                : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
                : "memory");
   (void)m0_out;
 }
 // (Dwords are the exponents'. Their row may end inside a load, so the whole
-// position is in the vector offset, which the descriptor checks.)
+// position is in the vector offset, which the descriptor checks. Their
+// descriptors are made just ahead: all five waits.)
 __device__ __forceinline__ void load_lds4_at(i32x4 rsrc, uint32_t lds_addr, uint32_t voff) {
   int m0_out;
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_dword %2, %3, %4 offen lds"
