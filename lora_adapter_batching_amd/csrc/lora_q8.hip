@@ -285,6 +285,9 @@ __global__ __launch_bounds__(kRowThreads) void swiglu_kernel(GateArgs a) {
   }
 }
 
+// dh meets sigma first: a closed gate's sigma then takes its size down before the
+// other factor can take the product out of fp32's range (dh u past 3.4e38 was
+// infinite, and times a sigma of 0 not a number).
 __device__ __forceinline__ void gate_grad(u32x4 g, u32x4 p, u32x4 d, float (&dg)[8], float (&dp)[8]) {
   float gf[8], pf[8], df[8];
   unpack8(g, gf);
@@ -293,8 +296,9 @@ __device__ __forceinline__ void gate_grad(u32x4 g, u32x4 p, u32x4 d, float (&dg)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float s = sigmoid(gf[i]);
-    dg[i] = df[i] * pf[i] * s * (1.f + gf[i] * (1.f - s));
-    dp[i] = df[i] * gf[i] * s;
+    const float t = df[i] * s;
+    dg[i] = t * pf[i] * (1.f + gf[i] * (1.f - s));
+    dp[i] = t * gf[i];
   }
 }
 

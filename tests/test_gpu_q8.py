@@ -755,3 +755,23 @@ def test_single_stored_row_of_any_stride():
     assert np.array_equal(to_f64(back), R.read_store(q))
     L.q8_matmul(q, w, y)
     check_matmul(q, w, y)
+
+
+def test_swiglu_backward_of_large_factors():
+    """Closed gates under gradients and rows so large that their product leaves fp32: the gradient itself is finite, and comes out so."""
+    g = np.array([-20, -40, -60, -80, -95, -110, -1, 2.0] * 2)
+    u = np.array([1e25, -1e25, 1e25, 1e30, -1e20, 1e20, 1e20, -3e10] + [1.0] * 8)
+    dh = np.array([1e20, 1e20, -1e20, 1e25, 1e20, 1e20, 1e17, 1e27] + [3e37, -3e37, 3e37, 3e37, 3e37, 3e38, 3e37, 1e37])
+    gu, d = bf16(np.stack([np.concatenate([g, u])] * 3)), bf16(np.stack([dh] * 3))
+    out, outq = torch.empty_like(gu), L.new_q8_rows(3, 32)
+    L.swiglu_backward(gu, d, out, outq)
+    g, u, s, _ = R.swiglu(to_f64(gu))
+    dh = to_f64(d)
+    ref = R.swiglu_grad(to_f64(gu), dh)
+    rel = (np.abs(g) + 10) * 2.0 ** -22
+    # (2^-126: sigma where it is not a normal number)
+    err = np.concatenate([np.abs(dh * u) * ((s * (1 + np.abs(g))) * (2 + np.abs(g)) * rel + (1 + np.abs(g)) * 2.0 ** -126),
+                          np.abs(dh * g) * (s * rel + 2.0 ** -126)], axis=1)
+    assert np.abs(dh * u).max() > 1e40 and np.abs(ref).max() < 3e38
+    held(to_f64(out), ref, BF * (np.abs(ref) + err) + err)
+    check_restored(outq, ref, err)
