@@ -643,5 +643,22 @@ def inspect_graph(num_adapters: int, h_in: int, h_out: int, max_rank: int, num_t
     return np.frombuffer(bytes(items), dtype=dt, count=int(n.value)).copy()
 
 
+class CMatmulKernel(ctypes.Structure):
+    """lora_matmul_kernel_t of the internal inspection entry (csrc/lora_inspect.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("kernels", "kernel", "tokens", "columns", "groups", "stages", "blocks", "exps")]
+
+
+def inspect_matmul(num_tokens: int, width: int, h_out: int) -> CMatmulKernel:
+    """Host-only: the kernel that q8_matmul launches for these sizes."""
+    lib = load()
+    fn = lib.lora_inspect_matmul
+    fn.restype = ctypes.c_int
+    fn.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(CMatmulKernel)]
+    out = CMatmulKernel()
+    _check(fn(int(num_tokens), int(width), int(h_out), ctypes.byref(out)))
+    return out
+
+
 def version() -> int:
     return int(load().lora_version())

@@ -83,6 +83,19 @@ int lora_inspect_plan(int op, int32_t num_proj, const lora_adapters_t* const* ad
 int lora_inspect_graph(const lora_graph_adapters_t* adapters, int32_t num_tokens, int32_t tiles, int32_t cus,
                        int32_t xccs, lora_plan_item_t* items, int64_t items_cap, int64_t* n_items);
 
+/* The kernel that lora_q8_matmul() launches for num_tokens rows of x, a sum
+ * over `width` columns and h_out columns of y. Host only. */
+typedef struct lora_matmul_kernel_t {
+  int32_t kernels;         /* number of kernels there are to choose from */
+  int32_t kernel;          /* the chosen one: 0 the few-token kernel, else a tile */
+  int32_t tokens, columns; /* of a workgroup's tile */
+  int32_t groups;          /* groups of waves (few tokens: waves) that share a tile's sum */
+  int32_t stages;          /* LDS stages of a group's ring (0: no ring) */
+  int32_t blocks;          /* 128-column blocks of the sum that a group walks */
+  int32_t exps;            /* blocks whose exponents LDS holds at a time (0: none are staged) */
+} lora_matmul_kernel_t;
+int lora_inspect_matmul(int32_t num_tokens, int32_t width, int32_t h_out, lora_matmul_kernel_t* out);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,6 +18,7 @@
 
 #include <type_traits>
 
+#include "lora_inspect.h"
 #include "lora_internal.h"
 #include "lora_q8.h"
 
@@ -527,38 +528,48 @@ void launch_few(const MatArgs& a, bool add, hipStream_t s) {
 //   37, 9728, 2560                    48        31       37      30      25     15     12
 // (* with three stages, one workgroup per CU; the other holds two)
 struct TileChoice {
-  int bt, bn, ks, slots;
+  int bt, bn, ks, stages, slots;
   float fixed, step;
   void (*launch)(MatArgs, bool, hipStream_t);
 };
+template <class C>
+constexpr TileChoice choice(int slots, float fixed, float step) {
+  return TileChoice{C::BT, C::BN, C::KS, C::S, slots, fixed, step, launch_tile<C>};
+}
 const TileChoice kTiles[] = {
-    {256, 256, 1, 256, 10.6f, 1.40f, launch_tile<Tile<256, 256, 2, 2, 2, 1, true>>},
-    {128, 128, 1, 512, 2.4f, 1.00f, launch_tile<Tile<128, 128, 2, 2, 2>>},
-    {128, 128, 1, 256, 6.2f, 0.34f, launch_tile<Tile<128, 128, 2, 2, 3>>},
-    {128, 160, 1, 256, 7.6f, 0.37f, launch_tile<Tile<128, 160, 4, 1, 3>>},
-    {128, 96, 1, 256, 6.3f, 0.26f, launch_tile<Tile<128, 96, 4, 1, 3>>},
-    {128, 64, 1, 256, 4.9f, 0.26f, launch_tile<Tile<128, 64, 2, 2, 3>>},
-    {32, 64, 4, 256, 3.4f, 0.56f, launch_tile<Tile<32, 64, 1, 2, 3, 4>>},
-    {32, 32, 4, 256, 3.1f, 0.39f, launch_tile<Tile<32, 32, 1, 1, 4, 4>>},
+    choice<Tile<256, 256, 2, 2, 2, 1, true>>(256, 10.6f, 1.40f),
+    choice<Tile<128, 128, 2, 2, 2>>(512, 2.4f, 1.00f),
+    choice<Tile<128, 128, 2, 2, 3>>(256, 6.2f, 0.34f),
+    choice<Tile<128, 160, 4, 1, 3>>(256, 7.6f, 0.37f),
+    choice<Tile<128, 96, 4, 1, 3>>(256, 6.3f, 0.26f),
+    choice<Tile<128, 64, 2, 2, 3>>(256, 4.9f, 0.26f),
+    choice<Tile<32, 64, 1, 2, 3, 4>>(256, 3.4f, 0.56f),
+    choice<Tile<32, 32, 1, 1, 4, 4>>(256, 3.1f, 0.39f),
 };
 
 constexpr int64_t kMaxTiles = 0xffffffffll / 512;
 
-void launch_matmul(const MatArgs& a, bool add, hipStream_t s) {
+// The tile for T tokens, N columns and a sum of nkb blocks; null: the few-token kernel.
+const TileChoice* choose(int32_t T, int32_t N, int32_t nkb) {
   // One matrix fragment of tokens: the weights' bytes are all that counts (one
   // token 2560 -> 2560: 4.0 us against 6.2 with 32 x 32 tiles, 2560 -> 19456: 11
   // against 13 with 128 x 96; 16 tokens 4.9 against 6.2 and 15 against 13, 9728 ->
   // 2560: 12 either way).
   // (A launch holds fewer than 2^32 threads, 512 of them per workgroup.)
-  if (a.T <= kFewTokens && a.N <= 1 << 26) return launch_few(a, add, s);
+  if (T <= kFewTokens && N <= 1 << 26) return nullptr;
   const TileChoice* best = &kTiles[0];  // (its grid is checked by the caller)
   double least = 0.;
   for (const TileChoice& c : kTiles) {
-    const int64_t tiles = ((int64_t)a.T + c.bt - 1) / c.bt * (((int64_t)a.N + c.bn - 1) / c.bn);
-    const double t = (double)((tiles + c.slots - 1) / c.slots) * (c.fixed + (double)c.step * ((a.nkb + c.ks - 1) / c.ks));
+    const int64_t tiles = ((int64_t)T + c.bt - 1) / c.bt * (((int64_t)N + c.bn - 1) / c.bn);
+    const double t = (double)((tiles + c.slots - 1) / c.slots) * (c.fixed + (double)c.step * ((nkb + c.ks - 1) / c.ks));
     if (&c == &kTiles[0] || (t < least && tiles <= kMaxTiles)) best = &c, least = t;
   }
-  best->launch(a, add, s);
+  return best;
+}
+
+void launch_matmul(const MatArgs& a, bool add, hipStream_t s) {
+  if (const TileChoice* c = choose(a.T, a.N, a.nkb)) c->launch(a, add, s);
+  else launch_few(a, add, s);
 }
 
 }  // namespace
@@ -597,3 +608,23 @@ extern "C" int lora_q8_matmul(const lora_q8_t* x, const lora_q8_t* w, void* y, i
   return LORA_OK;
 }
 #endif
+
+// Host-only: the kernel that a product takes (lora_inspect.h)
+extern "C" int lora_inspect_matmul(int32_t num_tokens, int32_t width, int32_t h_out, lora_matmul_kernel_t* out) {
+  clear_error();
+  if (!out) return set_error(LORA_INVALID_ARGUMENT, "out is NULL");
+  if (num_tokens <= 0 || width <= 0 || h_out <= 0 || (width & 7) || (h_out & 7))
+    return set_error(LORA_INVALID_ARGUMENT, "num_tokens (%d), width (%d) and h_out (%d) must be positive, the widths multiples of 8",
+                     num_tokens, width, h_out);
+  const int32_t nkb = (int32_t)q8_blocks(width);
+  const TileChoice* c = choose(num_tokens, h_out, nkb);
+  out->kernels = 1 + (int32_t)(sizeof(kTiles) / sizeof(kTiles[0]));
+  out->kernel = c ? 1 + (int32_t)(c - kTiles) : 0;
+  out->tokens = c ? c->bt : kFewTokens;
+  out->columns = c ? c->bn : 16;
+  out->groups = c ? c->ks : kFewWaves;
+  out->stages = c ? c->stages : 0;
+  out->blocks = (nkb + out->groups - 1) / out->groups;
+  out->exps = c ? kExpBlocks : 0;
+  return LORA_OK;
+}

@@ -13,6 +13,7 @@ import torch
 import lora_adapter_batching_amd as L
 from lora_adapter_batching_amd import binding as B
 from tests import q8_ref as R
+from tests.q8_products import PRODUCTS
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 1 << 40  # an aligned stand-in address, never read
@@ -308,3 +309,75 @@ def test_binding_takes_a_single_stored_row_of_any_stride():
                  (torch.zeros((256, 2), dtype=torch.uint8).t(), torch.zeros((2, 4), dtype=torch.uint8))]:
         with pytest.raises(ValueError):
             L.Q8Rows(v, e, 256)
+
+
+# Kernels of the product that no size takes with a sum behind the exponents it
+# holds: two-stage 128 x 128 tiles cost more than three-stage ones from 31 blocks.
+SHORT_SUMS_ONLY = {(128, 128, 2)}
+
+
+def test_every_kernel_of_the_product_is_reached_by_a_tested_size():
+    """The sizes that the GPU tests multiply take every kernel, ragged in each
+    direction, with short sums and with sums behind its staged exponents. The
+    choice is made from measured times, so another fit of them moves sizes from
+    one kernel to another: this says when the list has to follow."""
+    chosen = {}
+    for T, K, N in PRODUCTS:
+        k = B.inspect_matmul(T, K, N)
+        if k.stages:
+            assert T > k.tokens and N > k.columns, (T, K, N)     # more than one tile each way
+        assert T % k.tokens or not k.stages, (T, K, N)
+        assert N % k.columns and K % 128, (T, K, N)
+        chosen.setdefault(k.kernel, []).append(k)
+    assert sorted(chosen) == list(range(k.kernels))
+    for kernel, ks in chosen.items():
+        k = ks[0]
+        long = [q for q in ks if q.blocks > q.exps]
+        short = [q for q in ks if k.stages < q.blocks <= q.exps]
+        if k.stages == 0:
+            assert any(q.blocks > 1 for q in ks)
+        else:
+            assert short, (kernel, k.tokens, k.columns)
+            assert long or (k.tokens, k.columns, k.stages) in SHORT_SUMS_ONLY, (kernel, k.tokens, k.columns)
+
+
+def test_kernels_left_out_of_long_sums_never_take_one():
+    rng = np.random.default_rng(7)
+    for _ in range(20000):
+        T, N = int(2 ** rng.uniform(0, 20)), 8 * int(2 ** rng.uniform(0, 14))
+        k = B.inspect_matmul(T, 128 * int(rng.integers(61, 600)), N)
+        assert not (k.blocks > k.exps > 0 and (k.tokens, k.columns, k.stages) in SHORT_SUMS_ONLY)
+
+
+def test_matmul_inspection_refusals():
+    lib, out = L.load(), B.CMatmulKernel()
+    B.inspect_matmul(1, 8, 8)
+    for args in [(0, 8, 8, ctypes.byref(out)), (1, 0, 8, ctypes.byref(out)), (1, 8, 0, ctypes.byref(out)), (1, 12, 8, ctypes.byref(out)),
+                 (1, 8, 12, ctypes.byref(out)), (1, 8, 8, None)]:
+        assert lib.lora_inspect_matmul(*args) == B.LORA_INVALID_ARGUMENT
+
+
+def test_whole_number_products_show_any_misplaced_part():
+    """What the GPU test of every kernel compares: with a mistake planted in
+    the 64-bit form, y differs in every 32 x 32 fragment that it touches."""
+    from tests.test_gpu_q8_products import exact_case
+    T, K, N = 96, 1352, 264
+    x, w, y0, ref, y064 = exact_case(T, K, N, 1, "cpu")
+    xq, xe = R.quantize(x.double().numpy())
+    wq, we = R.quantize(w.double().numpy(), 128)
+    want = ref.float().to(torch.bfloat16)
+    product = lambda a, b: torch.from_numpy(a @ b.T).float().to(torch.bfloat16)  # noqa: E731
+    xs, ws = R.restore(xq, xe), R.restore(wq, we, 128)
+    assert torch.equal(product(xs, ws), want)                    # the operands are exact, and so is the product
+    same = lambda got: (got == want)[:96, :256].reshape(3, 32, 8, 32).all(3).all(1)  # noqa: E731
+    for b in range(11):
+        gone = ws.copy()
+        gone[:, 128 * b:128 * b + 128] = 0                       # block b left out
+        assert not same(product(xs, gone)).any(), b
+    for b in range(10):
+        turned = xe.copy()
+        turned[:, [b, b + 1]] = turned[:, [b + 1, b]]            # two blocks' exponents exchanged
+        if (xe[:, b] != xe[:, b + 1]).all():
+            assert not same(product(R.restore(xq, turned), ws)).any(), b
+    assert not same(torch.roll(want, 1, 1)).any() and not same(torch.roll(want, 1, 0)).any()
+    assert not same((ref + y064).float().to(torch.bfloat16)).any()
