@@ -18,7 +18,7 @@ import torch
 import lora_adapter_batching_amd as L
 from tests import q8_ref as R
 from tests.q8_products import PRODUCTS
-from tests.test_gpu_q8 import strided, wide_q8
+from tests.test_gpu_q8 import LONG, strided, wide_q8
 
 pytestmark = pytest.mark.gpu
 
@@ -88,8 +88,10 @@ def values64(q):
     return v, torch.where(v == 0, torch.zeros((), dtype=torch.float64, device="cuda"), top)
 
 
-# The tolerance of test_gpu_q8.py's check_matmul, over every column.
-@pytest.mark.parametrize("T,K,N", PRODUCTS)
+# The tolerance of test_gpu_q8.py's check_matmul, over every column; also of the
+# sizes that its test of long sums compares in some columns and in row sums,
+# whose limit a tile of zeros stays below.
+@pytest.mark.parametrize("T,K,N", PRODUCTS + LONG)
 def test_every_kernel_on_random_values(T, K, N):
     g = torch.Generator(device="cuda")
     g.manual_seed(T * K + N)
