@@ -775,3 +775,56 @@ def test_swiglu_backward_of_large_factors():
     assert np.abs(dh * u).max() > 1e40 and np.abs(ref).max() < 3e38
     held(to_f64(out), ref, BF * (np.abs(ref) + err) + err)
     check_restored(outq, ref, err)
+
+
+# ---------------------------------------------------------------------------
+# Large batches of the gated activation (2^20 chunks of 8 columns and more:
+# several chunks per thread, accesses past the caches)
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("F", [9736, 9728])
+@pytest.mark.parametrize("form", ["bf16", "q8", "both"])
+def test_swiglu_large_batch(F, form):
+    """Chunks past 2^20, in a number that leaves the last workgroup part empty."""
+    T = 901
+    chunks = T * (F // 8 if form == "bf16" else R.padded(F) // 8)
+    assert chunks >= 1 << 20 and chunks % 512
+    rng = np.random.default_rng(F)
+    gu = gates(rng, T, F)
+    big, h = strided(torch.zeros((T, F), dtype=torch.bfloat16, device="cuda"))
+    hq = wide_q8(T, F)
+    L.swiglu(strided(gu)[1], h if form != "q8" else None, hq if form != "bf16" else None)
+    g, u, s, ref = R.swiglu(to_f64(gu))
+    err = np.abs(ref) * (np.abs(g) + 8) * 2.0 ** -22 + np.abs(g * u) * 2.0 ** -126
+    if form != "q8":
+        held(to_f64(h), ref, BF * (np.abs(ref) + err) + err)
+        assert torch.all(big[T] == 7) and torch.all(big[:, F:] == 7)
+    if form != "bf16":
+        check_restored(hq, ref, err)
+        b = hq.values.cpu().numpy()
+        assert not b[:T, F:R.padded(F)].any() and np.all(b[T] == 0xAB) and np.all(b[:, R.padded(F):] == 0xAB)
+
+
+@pytest.mark.parametrize("F", [9728, 9736])
+@pytest.mark.parametrize("form", ["bf16", "q8", "both"])
+def test_swiglu_backward_large_batch(F, form):
+    """The same for the gradient: whole blocks in each half (9728), and a block that holds the end of one and the start of the other (9736)."""
+    T = 901
+    assert T * (F // 8) >= 1 << 20 and T * (F // 8) % 256
+    rng = np.random.default_rng(F)
+    gu, dh = gates(rng, T, F), rows(rng, T, F)
+    big, d = strided(torch.zeros((T, 2 * F), dtype=torch.bfloat16, device="cuda"))
+    dq = wide_q8(T, 2 * F)
+    L.swiglu_backward(strided(gu)[1], strided(dh)[1], d if form != "q8" else None, dq if form != "bf16" else None)
+    g, u, s, _ = R.swiglu(to_f64(gu))
+    dh64 = to_f64(dh)
+    ref = R.swiglu_grad(to_f64(gu), dh64)
+    rel = (np.abs(g) + 10) * 2.0 ** -22
+    err = np.concatenate([np.abs(dh64 * u) * ((s * (1 + np.abs(g))) * (2 + np.abs(g)) * rel + (1 + np.abs(g)) * 2.0 ** -126),
+                          np.abs(dh64 * g) * (s * rel + 2.0 ** -126)], axis=1)
+    if form != "q8":
+        held(to_f64(d), ref, BF * (np.abs(ref) + err) + err)
+        assert torch.all(big[T] == 7) and torch.all(big[:, 2 * F:] == 7)
+    if form != "bf16":
+        check_restored(dq, ref, err)
+        b = dq.values.cpu().numpy()
+        assert not b[:T, 2 * F:R.padded(2 * F)].any() and np.all(b[T] == 0xAB) and np.all(b[:, R.padded(2 * F):] == 0xAB)
