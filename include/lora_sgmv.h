@@ -347,8 +347,9 @@ int lora_packed_backward(const void* x, int64_t ldx, const void* dy, int64_t ldd
  * weights). A scale is a power of two, kept as its biased exponent:
  *     value(i, j) = e4m3(values[i * ld + j])
  *                   * 2^(exps[(i / block_rows) * ld_exps + j / 128] - 127)
- * Stored exponents are 1..253; other bytes do not fault, but their values are
- * unspecified. Rows are stored in whole blocks: the bytes of the last block
+ * Exponents 1..253 are read as that; other bytes do not fault, but their values
+ * are unspecified. The writing calls store 1..247 (the scale of the largest
+ * finite value). Rows are stored in whole blocks: the bytes of the last block
  * behind `width` belong to the matrix and must be zero in what a product
  * reads (lora_q8_quantize() and the other writing calls store zeros there).
  * The struct itself is HOST memory, read during the call only.

@@ -9,8 +9,7 @@
 
 namespace lora {
 
-constexpr int kQ8Block = 128;      // columns that share one scale
-constexpr int kQ8MaxExp = 253;     // biased exponents the quantiser writes: 1 .. 253
+constexpr int kQ8Block = 128;  // columns that share one scale
 
 inline int64_t q8_blocks(int64_t width) { return (width + kQ8Block - 1) / kQ8Block; }
 
@@ -27,7 +26,8 @@ __device__ __forceinline__ float q8_scale(uint32_t e) { return __builtin_bit_cas
 // Smallest biased exponent e >= 1 with m <= 448 * 2^(e - 127), for the
 // largest finite magnitude m of a block. 448 = 1.75 * 2^8, so e is m's own
 // exponent field less 8, and one more where the fraction is above 0.75.
-// Subnormal m (exponent field 0) and m = 0 end at the lower clamp.
+// Subnormal m (exponent field 0) and m = 0 end at the lower clamp; the largest
+// finite m (field 254) gives 247.
 __device__ __forceinline__ uint32_t q8_exponent(float m) {
   const uint32_t b = __builtin_bit_cast(uint32_t, m);
   const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);

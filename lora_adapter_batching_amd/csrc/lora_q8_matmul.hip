@@ -575,7 +575,6 @@ void launch_matmul(const MatArgs& a, bool add, hipStream_t s) {
 }  // namespace
 }  // namespace lora
 
-#ifndef LORA_Q8_KERNELS_ONLY
 using namespace lora;
 
 extern "C" int lora_q8_matmul(const lora_q8_t* x, const lora_q8_t* w, void* y, int64_t ldy, uint32_t flags, void* stream) {
@@ -607,7 +606,6 @@ extern "C" int lora_q8_matmul(const lora_q8_t* x, const lora_q8_t* w, void* y, i
   if (e != hipSuccess) return set_error(LORA_DEVICE_ERROR, "q8_matmul launch failed: %s", hipGetErrorString(e));
   return LORA_OK;
 }
-#endif
 
 // Host-only: the kernel that a product takes (lora_inspect.h)
 extern "C" int lora_inspect_matmul(int32_t num_tokens, int32_t width, int32_t h_out, lora_matmul_kernel_t* out) {

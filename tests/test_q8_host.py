@@ -381,3 +381,9 @@ def test_whole_number_products_show_any_misplaced_part():
             assert not same(product(R.restore(xq, turned), ws)).any(), b
     assert not same(torch.roll(want, 1, 1)).any() and not same(torch.roll(want, 1, 0)).any()
     assert not same((ref + y064).float().to(torch.bfloat16)).any()
+
+
+def test_written_exponents_end_at_the_largest_finite_values():
+    """The header's range of stored exponents: 1 for zeros and subnormals, 247 for the largest fp32 and bf16 values."""
+    top = np.array([[np.finfo(np.float32).max], [float(torch.finfo(torch.bfloat16).max)], [2.0 ** -149], [0.0]])
+    assert R.block_exponents(top, 1)[:, 0].tolist() == [247, 247, 1, 1]
