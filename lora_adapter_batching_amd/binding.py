@@ -474,6 +474,9 @@ def _q8_arg(name: str, q: _Q8, dev: int) -> int:
     return q.addr
 
 
+_INDEX_TYPES, _ADDRESS_TYPES = ("torch.int32",), ("torch.int64", "torch.uint64")
+
+
 def _largest_rank(adapters: Adapters, segments: Segments) -> int:
     used = segments.seg_adapter[(segments.seg_adapter >= 0) & (segments.seg_adapter < len(adapters.ranks))]
     return int(adapters.ranks[used].max(initial=0))
@@ -542,6 +545,12 @@ def packed_backward_q8(x: Q8Rows, dy, u, adapters: Adapters, segments: Segments,
                     ("dB_ptrs", dB_ptrs), ("ws", ws)):
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, expected {_dev_name(dev)}")
+    # tables that the kernels index: a shorter or narrower one would be read behind its end
+    for name, t, n, types in (("token_rows", segments.token_rows, T, _INDEX_TYPES),
+                              ("dA_ptrs", dA_ptrs, len(adapters.ranks), _ADDRESS_TYPES),
+                              ("dB_ptrs", dB_ptrs, len(adapters.ranks), _ADDRESS_TYPES)):
+        if t is not None and (str(t.dtype) not in types or t.numel() < n or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {types[0]} tensor of {n} entries, got {t.dtype} {tuple(t.shape)}")
     wp, wb = _ws(ws)
     _call_on(dev, stream, lib.lora_packed_backward_q8, x.addr, dy.data_ptr(), lddy, u.data_ptr(), ldu,
              adapters.c, segments.c, _ptr(dx), lddx, _ptr(dA_ptrs), _ptr(dB_ptrs), int(flags), wp, wb)

@@ -387,3 +387,26 @@ def test_written_exponents_end_at_the_largest_finite_values():
     """The header's range of stored exponents: 1 for zeros and subnormals, 247 for the largest fp32 and bf16 values."""
     top = np.array([[np.finfo(np.float32).max], [float(torch.finfo(torch.bfloat16).max)], [2.0 ** -149], [0.0]])
     assert R.block_exponents(top, 1)[:, 0].tolist() == [247, 247, 1, 1]
+
+
+def test_binding_refuses_tables_that_the_kernels_would_overrun():
+    """Row and address tables of another type, shorter than the batch or the adapters, or with gaps."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    ad = L.Adapters([bf(8, 256), bf(8, 256)], [bf(64, 8), bf(64, 8)], [8, 8], [1.0, 1.0], 256, 64, device="cpu")
+    q, dy, u = L.new_q8_rows(4, 256, "cpu"), bf(4, 64), torch.zeros((4, 8))
+    tab, rows_ = torch.zeros(2, dtype=torch.int64), torch.arange(4, dtype=torch.int32)
+
+    def call(rows=None, a=tab, b=tab):
+        L.packed_backward_q8(q, dy, u, ad, L.Segments([0, 2, 4], [0, 1], rows), None, a, b)
+
+    for rows in (rows_.long(), rows_[:3], torch.arange(8, dtype=torch.int32)[::2], rows_.short()):
+        with pytest.raises(ValueError, match="token_rows must be"):
+            call(rows)
+    for bad in (tab.int(), tab[:1], torch.zeros(4, dtype=torch.int64)[::2], tab.double()):
+        with pytest.raises(ValueError, match="dA_ptrs must be"):
+            call(a=bad)
+        with pytest.raises(ValueError, match="dB_ptrs must be"):
+            call(b=bad)
+    for ok in (dict(), dict(rows=rows_), dict(a=torch.zeros(3, dtype=torch.int64), b=tab.view(torch.uint64))):
+        with pytest.raises(ValueError, match="device tensors"):
+            call(**ok)
