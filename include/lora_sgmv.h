@@ -41,7 +41,8 @@
  *    enqueue work and never synchronise the device. Calls must not be
  *    captured into a HIP graph (each launch carries a fresh hand-off id in
  *    its kernel argument, which a replayed graph would repeat), except
- *    lora_sgmv_fused_graph(), which takes its id from the device.
+ *    lora_sgmv_fused_graph(), which takes its id from the device, and the
+ *    calls without hand-off whose comment says that they can be.
  *  - Workspace: size it with lora_workspace_size(). It must be filled with
  *    zero bytes once before its first use; every call returns its counters
  *    to zero when its work completes. The hand-off stamps a call leaves in
@@ -402,10 +403,12 @@ int lora_q8_matmul(const lora_q8_t* x, const lora_q8_t* w, void* y, int64_t ldy,
  * 1) of the projection's input, so dA_i = sum_p du[p] x(row(p))^T is over
  * the stored values. u is the forward's own (u_save of lora_sgmv_fused) and
  * required: it came from the unrounded x, so dB, du and dx are those of
- * lora_packed_backward(). x->width = h_in; x->rows must cover every row the
- * segments name (rows outside [0, x->rows) read as zero). Everything else,
- * the workspace (LORA_OP_BACKWARD) among it, is as there. A stream that is
- * being captured is refused (LORA_INVALID_ARGUMENT).
+ * lora_packed_backward(). u and du enter dB and dA with all their 24 bits; in
+ * dx += A_i^T du[p], as there, du enters as two bf16 parts (up to 2^-16 of it
+ * is left out, below dx's own bf16 rounding). x->width = h_in; x->rows must
+ * cover every row the segments name (rows outside [0, x->rows) read as zero).
+ * Everything else, the workspace (LORA_OP_BACKWARD) among it, is as there. A
+ * stream that is being captured is refused (LORA_INVALID_ARGUMENT).
  */
 int lora_packed_backward_q8(const lora_q8_t* x, const void* dy, int64_t lddy, const float* u, int64_t ldu,
                             const lora_adapters_t* adapters, const lora_segments_t* segments, void* dx,
@@ -419,7 +422,9 @@ int lora_packed_backward_q8(const lora_q8_t* x, const void* dy, int64_t lddy, co
  *     h = g * sigma(g) * u
  * is written as bf16 rows (h, or NULL) and/or straight into the 8-bit rows
  * that the down projection reads (hq, or NULL; block_rows = 1); each output
- * is rounded once from fp32. The backward gives, for dh [num_tokens, width],
+ * is rounded once from fp32. sigma comes from the hardware's exp2 and
+ * reciprocal: it is within (|g| + 6) 2^-22 of its value, and may be 0 where
+ * that is below 2^-126. The backward gives, for dh [num_tokens, width],
  *     dg = dh * u * sigma(g) * (1 + g (1 - sigma(g))),   du = dh * g * sigma(g)
  * as one [num_tokens, 2 width] matrix in the same two forms. Rounded to 8
  * bits, dgate_up is what the gate_up projection's dx = dy W reads.

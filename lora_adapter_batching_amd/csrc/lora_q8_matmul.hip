@@ -138,8 +138,10 @@ __device__ __forceinline__ void tile_of(const MatArgs& a, int b, int grid, int& 
 //    same time, and 4 MB of y an XCD would push the rows of the next tiles out of
 //    its L2 (395 us without). Smaller tiles keep plain stores: their y
 //    is small and the next operator reads it.
-// Now 355-371 us, 2.6-2.7 PFLOP/s (the library's fp8 product without block scales:
-// 384). The steps run at 3.0; the rest is each tile's start and end (6 us of 52).
+// Now 350-371 us by card, 2.6-2.75 PFLOP/s; where it takes 350-353, the library's fp8
+// product without block scales, called in turn in the same process on inputs of the
+// same distribution, takes 311-313 (8191 tokens 4096 -> 4096: 106-109 and 93-99). The
+// steps run at 3.0 PFLOP/s; the rest is each tile's start and end (6 us of 52).
 // ---------------------------------------------------------------------------
 template <int BT_, int BN_, int WT_, int WN_, int S_, int KS_ = 1, bool STREAM_ = false>
 struct Tile {
@@ -440,10 +442,14 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
 // Few tokens: the weights are read once and that is the floor. A workgroup
 // owns 16 columns and up to 16 tokens; its 8 waves take every eighth block of
 // the sum straight from memory into fragments (no LDS on the way, each w row in
-// whole 128-byte lines) and their parts are added in wave order. Eight small
-// workgroups a CU hide the latency: two to four blocks in flight per wave, or
-// 16 waves, were no faster. One token 2560 -> 2560 4.0 us, 2560 -> 19456 10.9 us
-// (4.6 TB/s), 9728 -> 2560 8.6 us.
+// whole 128-byte lines) and their parts are added in wave order. A CU holds four
+// such workgroups. Wide projections have that many to hide the latency: one token
+// 2560 -> 19456 10.4 us (4.8 TB/s), 16 tokens 14.7. 2560 columns are 160
+// workgroups, less than one a CU, and then a wave's blocks follow each other, one
+// load's latency each: one token 2560 -> 2560 4.0-4.6 us (three blocks a wave at
+// most), 9728 -> 2560 8.2 (ten; its bytes take 4.8), 16 tokens 11.3. Two to four
+// blocks in flight per wave, or 16 waves, were no faster; the sum is not divided
+// over workgroups, which would need a workspace or a second launch.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
 constexpr int kFewTokens = 16;
@@ -527,6 +533,11 @@ void launch_few(const MatArgs& a, bool add, hipStream_t s) {
 //   100, 9728, 2560                   51        32       38      30      25     15     21
 //   37, 9728, 2560                    48        31       37      30      25     15     12
 // (* with three stages, one workgroup per CU; the other holds two)
+// The costs are a fit, and read low where a three-stage tile needs several rounds
+// (128x128* at 8191 tokens 137 for 160, at 2048 34 for 40) and high for one round
+// of 256x256 (55 for 45), and nothing in them stands for the weights' bytes. Where
+// two tiles are near each other the choice can then be the slower one: of the
+// sizes above, 2048 tokens 4096 -> 4096 takes 128x128* (40) over 128x128 (35).
 struct TileChoice {
   int bt, bn, ks, stages, slots;
   float fixed, step;
@@ -553,8 +564,9 @@ constexpr int64_t kMaxTiles = 0xffffffffll / 512;
 const TileChoice* choose(int32_t T, int32_t N, int32_t nkb) {
   // One matrix fragment of tokens: the weights' bytes are all that counts (one
   // token 2560 -> 2560: 4.0 us against 6.2 with 32 x 32 tiles, 2560 -> 19456: 11
-  // against 13 with 128 x 96; 16 tokens 4.9 against 6.2 and 15 against 13, 9728 ->
-  // 2560: 12 either way).
+  // against 13 with 128 x 96; 16 tokens 2560 -> 2560 4.9 against 6.2, 9728 -> 2560
+  // 12 either way). The one measured size that it loses is 16 tokens 2560 -> 19456,
+  // 15 against 13: the border stays at the fragment's rows.
   // (A launch holds fewer than 2^32 threads, 512 of them per workgroup.)
   if (T <= kFewTokens && N <= 1 << 26) return nullptr;
   const TileChoice* best = &kTiles[0];  // (its grid is checked by the caller)
