@@ -9,6 +9,9 @@ hipcc cross-compiles the device code to assembly; no GPU needed).
 - The output rows y are streamed: every 16-byte buffer store of the forward
   kernels (the y stores) carries the non-temporal bit, and so do the x loads
   of one-item-per-tile launches (a second form of the LDS-destination load).
+- M0 and scalar registers that vector instructions wrote have aged the wait
+  states that an LDS-destination load needs (one and five): the compiler does
+  not insert them inside inline assembly.
 """
 import os
 import re
