@@ -437,6 +437,67 @@ int lora_swiglu(const void* gate_up, int64_t ld, int32_t num_tokens, int32_t wid
 int lora_swiglu_backward(const void* gate_up, int64_t ld, const void* dh, int64_t lddh, int32_t num_tokens,
                          int32_t width, void* dgate_up, int64_t lddg, const lora_q8_t* dgate_up_q, void* stream);
 
+/*
+ * 4-bit rows and weights: a frozen base at half the bytes of the 8-bit form
+ * and, where both operands are in 4 bits, at twice its matrix rate. A matrix
+ * [rows, width] is e2m1 (1 sign, 2 exponent, 1 mantissa bit: 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6) with one power-of-two scale per 32 columns of one row. Columns
+ * are held in panels of 128, each with the 64 bytes of every row behind each
+ * other, so that the product reads whole runs of memory:
+ *     code(i, j)  = half j % 2 (0: low) of values[(j / 128) * ld + 64 * i + (j % 128) / 2]
+ *     value(i, j) = e2m1(code) * 2^(exps[(j / 128) * ld_exps + 4 * i + (j % 128) / 32] - 127)
+ * Exponents 1..253 are read as that, and 255 makes its 32 values NaN; other
+ * bytes do not fault, but their values are unspecified. The last panel is
+ * stored whole: what lies behind `width` belongs to the matrix, and in what a
+ * product reads its codes must be zero and its exponents below 255 (the
+ * writing calls store codes 0 and exponents 1). Rows i0 .. of a matrix are the
+ * matrix at values + 64 i0 and exps + 4 i0 with the same strides.
+ * The struct itself is HOST memory, read during the call only.
+ */
+typedef struct lora_q4_t {
+  uint8_t* values;  /* DEVICE [ceil(width / 128)] panels of rows x 64 bytes, 16-byte aligned */
+  int64_t ld;       /* bytes between panels: a multiple of 16, >= 64 * rows */
+  uint8_t* exps;    /* DEVICE [ceil(width / 128)] panels of rows x 4 bytes, 4-byte aligned */
+  int64_t ld_exps;  /* bytes between exponent panels: a multiple of 4, >= 4 * rows */
+  int32_t rows;     /* >= 0 */
+  int32_t width;    /* a positive multiple of 8 */
+} lora_q4_t;
+
+/*
+ * Stores bf16 x [out->rows, out->width] in 4 bits. A block's scale is the
+ * smallest power of two s >= 2^-126 with max|x| <= 6 s; values are x / s
+ * (exact) rounded to the nearest code, ties to the even one. A block that
+ * holds NaN or an infinity gets the exponent 255: e2m1 has neither, and the
+ * block is NaN as a whole. out_t (NULL, or a store of width = out->rows and
+ * rows = out->width, both then multiples of 8) receives the transposed matrix
+ * in the same pass, the weights of the gradient's product dx = dy W. Each
+ * scale is then that of 32 rows x 32 columns, so that both stores hold the
+ * same values and dx is the gradient of the forward's own product; without
+ * out_t the blocks are 1 x 32. The buffers must not overlap. Can be captured
+ * into a HIP graph.
+ */
+int lora_q4_quantize(const void* x, int64_t ldx, const lora_q4_t* out, const lora_q4_t* out_t, void* stream);
+
+/* Restores q to bf16 x [q->rows, q->width] (exact wherever the value is a
+ * normal bf16 number; values past the type's range become infinities). Can be
+ * captured into a HIP graph. */
+int lora_q4_dequantize(const lora_q4_t* q, void* x, int64_t ldx, void* stream);
+
+/*
+ * The frozen projection on 4-bit weights:
+ *     y[t][j] = sum_k x(t, k) w(j, k)          for j < w->rows, t < x->rows
+ * (with LORA_MATMUL_ACCUMULATE: y[t][j] += ...), summed in fp32 and rounded
+ * once to bf16. x is in 4 bits, or (lora_q4_matmul_q8) 8-bit rows with
+ * block_rows = 1, as lora_q8_quantize() and lora_swiglu() write them: half the
+ * weights' bytes of lora_q8_matmul() at its matrix rate. The backward is the
+ * same call on dy and the transposed store: dx = dy W. Rules and limits are
+ * those of lora_q8_matmul(): widths agree, w->rows is a multiple of 8, y must
+ * not overlap the operands, no workspace, results that do not depend on
+ * scheduling, capturable; row strides of 8-bit rows are limited to 8 MB.
+ */
+int lora_q4_matmul(const lora_q4_t* x, const lora_q4_t* w, void* y, int64_t ldy, uint32_t flags, void* stream);
+int lora_q4_matmul_q8(const lora_q8_t* x, const lora_q4_t* w, void* y, int64_t ldy, uint32_t flags, void* stream);
+
 /* Static text for a status code. */
 const char* lora_status_string(int status);
 

@@ -15,9 +15,11 @@ from .binding import (  # noqa: F401
     OP_EXPAND,
     OP_FUSED,
     OP_SHRINK,
+    Q4,
     Q8Rows,
     Q8Weights,
     load,
+    new_q4,
     new_q8_rows,
     new_q8_weights,
     new_workspace,
@@ -25,6 +27,9 @@ from .binding import (  # noqa: F401
     new_workspace_multi,
     packed_backward,
     packed_backward_q8,
+    q4_dequantize,
+    q4_matmul,
+    q4_quantize,
     q8_dequantize,
     q8_matmul,
     q8_quantize,

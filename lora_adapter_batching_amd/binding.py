@@ -58,11 +58,17 @@ class CQ8(ctypes.Structure):
                 ("block_rows", ctypes.c_int32)]
 
 
+class CQ4(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("ld", ctypes.c_int64), ("exps", ctypes.c_void_p),
+                ("ld_exps", ctypes.c_int64), ("rows", ctypes.c_int32), ("width", ctypes.c_int32)]
+
+
 EXPORTS = ["lora_segments_from_ids", "lora_workspace_size", "lora_sgmv_shrink", "lora_sgmv_expand",
            "lora_sgmv_fused", "lora_packed_backward", "lora_workspace_size_multi",
            "lora_sgmv_fused_multi", "lora_sgmv_fused_noalloc", "lora_workspace_size_graph",
            "lora_sgmv_fused_graph", "lora_q8_quantize", "lora_q8_dequantize", "lora_q8_matmul",
-           "lora_packed_backward_q8", "lora_swiglu", "lora_swiglu_backward", "lora_status_string", "lora_last_error", "lora_version"]
+           "lora_packed_backward_q8", "lora_swiglu", "lora_swiglu_backward", "lora_q4_quantize", "lora_q4_dequantize",
+           "lora_q4_matmul", "lora_q4_matmul_q8", "lora_status_string", "lora_last_error", "lora_version"]
 NOALLOC_SCRATCH_BYTES = 16 << 20  # LORA_NOALLOC_SCRATCH_BYTES
 
 _lib = None
@@ -115,6 +121,10 @@ def load(path: str = LIB_PATH):
                                             P, I64, P, P, ctypes.c_uint32, P, ctypes.c_size_t, P]
     lib.lora_swiglu.argtypes = [P, I64, ctypes.c_int32, ctypes.c_int32, P, I64, Q, P]
     lib.lora_swiglu_backward.argtypes = [P, I64, P, I64, ctypes.c_int32, ctypes.c_int32, P, I64, Q, P]
+    lib.lora_q4_quantize.argtypes = [P, I64, P, P, P]  # (a CQ4 by its address, as a CQ8)
+    lib.lora_q4_dequantize.argtypes = [P, P, I64, P]
+    lib.lora_q4_matmul.argtypes = [P, P, P, I64, ctypes.c_uint32, P]
+    lib.lora_q4_matmul_q8.argtypes = [Q, P, P, I64, ctypes.c_uint32, P]
     lib.lora_status_string.restype = ctypes.c_char_p
     lib.lora_status_string.argtypes = [ctypes.c_int]
     lib.lora_last_error.restype = ctypes.c_char_p
@@ -468,7 +478,7 @@ def _rows_arg(name: str, t, rows: int, width: int, dev: int) -> int:
                      f"{_dev_name(dev)}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _q8_arg(name: str, q: _Q8, dev: int) -> int:
+def _q8_arg(name: str, q, dev: int) -> int:
     if q.dev != dev:
         raise ValueError(f"{name} is on {_dev_name(q.dev)}, expected {_dev_name(dev)}")
     return q.addr
@@ -578,6 +588,73 @@ def swiglu_backward(gate_up, dh, dgate_up=None, dgate_up_q: Optional[Q8Rows] = N
     q = _q8_arg("dgate_up_q", dgate_up_q, dev) if dgate_up_q is not None else None
     _call_on(dev, stream, lib.lora_swiglu_backward, gate_up.data_ptr(), ld, dh.data_ptr(), lddh, T, F,
              _ptr(dgate_up), ldd, q)
+
+
+# ---------------------------------------------------------------------------
+# 4-bit rows and weights and the frozen projection on them
+# ---------------------------------------------------------------------------
+class Q4:
+    """A matrix in 4 bits, rows or weights: e2m1 codes in panels of 128 columns,
+    uint8 [panels, >= rows, 64], and biased power-of-two exponents, one per 32
+    columns of a row, uint8 [panels, >= rows, 4]."""
+
+    def __init__(self, values, exps, width: int, rows: Optional[int] = None):
+        import torch
+        self.width = int(width)
+        panels = -(-self.width // 128)
+        for name, t, n in (("values", values, 64), ("exps", exps, 4)):
+            if t.dtype != torch.uint8 or t.dim() != 3 or t.shape[2] != n:
+                raise ValueError(f"{name} must be a uint8 [panels, rows, {n}] tensor, got {t.dtype} {tuple(t.shape)}")
+        self.rows = int(values.shape[1] if rows is None else rows)
+        lds = []
+        for name, t, n in (("values", values, 64), ("exps", exps, 4)):
+            if self.rows < 0 or t.shape[0] < panels or t.shape[1] < self.rows:
+                raise ValueError(f"{name} of shape {tuple(t.shape)} do not hold {self.rows} rows of {self.width} columns")
+            if self.rows and (t.stride(2) != 1 or self.rows > 1 and t.stride(1) != n):
+                raise ValueError(f"{name}: the rows of a panel must follow each other, got strides {t.stride()}")
+            # (a panel that no other follows may have any stride)
+            lds.append(t.stride(0) if panels > 1 and self.rows else n * max(1, self.rows))
+        if values.device != exps.device:
+            raise ValueError(f"values are on {values.device}, exps on {exps.device}")
+        self.values, self.exps = values, exps
+        self.dev = values.get_device()
+        self._c = CQ4(_ptr(values), lds[0], _ptr(exps), lds[1], self.rows, self.width)
+        self.addr = ctypes.addressof(self._c)
+
+
+def new_q4(rows: int, width: int, device="cuda") -> Q4:
+    import torch
+    panels = -(-int(width) // 128)
+    v = torch.empty((panels, int(rows), 64), dtype=torch.uint8, device=device)
+    e = torch.empty((panels, int(rows), 4), dtype=torch.uint8, device=device)
+    return Q4(v, e, width)
+
+
+def q4_quantize(x, out: Q4, out_t: Optional[Q4] = None, stream=None):
+    """Stores bf16 x in 4 bits; with out_t the transposed matrix too, scales
+    then shared by 32 x 32 values so that both hold the same numbers."""
+    lib, dev = _lib or load(), out.dev
+    ldx = _rows_arg("x", x, out.rows, out.width, dev)
+    ot = _q8_arg("out_t", out_t, dev) if out_t is not None else None
+    _call_on(dev, stream, lib.lora_q4_quantize, x.data_ptr(), ldx, out.addr, ot)
+
+
+def q4_dequantize(q: Q4, x, stream=None):
+    """Restores a 4-bit matrix to bf16 x."""
+    lib = _lib or load()
+    ldx = _rows_arg("x", x, q.rows, q.width, q.dev)
+    _call_on(q.dev, stream, lib.lora_q4_dequantize, q.addr, x.data_ptr(), ldx)
+
+
+def q4_matmul(x, w: Q4, y, accumulate: bool = False, stream=None):
+    """y = x w^T (or y += x w^T) on 4-bit weights; x in 4 bits (Q4) or 8-bit
+    rows (Q8Rows); y bf16 [x.rows, w.rows]."""
+    lib, dev = _lib or load(), x.dev
+    if not isinstance(w, Q4) or not isinstance(x, (Q4, Q8Rows)):
+        raise ValueError(f"q4_matmul takes Q4 or Q8Rows on Q4, got {type(x).__name__} on {type(w).__name__}")
+    fn = lib.lora_q4_matmul if isinstance(x, Q4) else lib.lora_q4_matmul_q8
+    ldy = _rows_arg("y", y, x.rows, w.rows, dev)
+    _call_on(dev, stream, fn, x.addr, _q8_arg("w", w, dev), y.data_ptr(), ldy, 1 if accumulate else 0)
 
 
 class CPlanItem(ctypes.Structure):
