@@ -498,6 +498,60 @@ int lora_q4_dequantize(const lora_q4_t* q, void* x, int64_t ldx, void* stream);
 int lora_q4_matmul(const lora_q4_t* x, const lora_q4_t* w, void* y, int64_t ldy, uint32_t flags, void* stream);
 int lora_q4_matmul_q8(const lora_q8_t* x, const lora_q4_t* w, void* y, int64_t ldy, uint32_t flags, void* stream);
 
+/*
+ * What the q and k projections' rows go through next (the norm of queries and
+ * keys and the rotation by position), in one pass: for every head x of token t
+ * and its kind's weight w,
+ *     r = 1 / sqrt(mean(x^2) + eps),   n = x r w,   a_i = positions[t] * freqs[i],
+ *     out_i = n_i cos a_i - n_j sin a_i,   out_j = n_j cos a_i + n_i sin a_i
+ * over the pairs (i, j) = (i, i + rot_dim / 2) of the head's first rot_dim
+ * columns, or the neighbours (2 i, 2 i + 1); the other columns of n pass
+ * unturned. Everything is in fp32 and rounded once to bf16, but for the
+ * angles: those are taken in 64 bits and reduced to part of a turn first, so
+ * far positions keep their digits. A head's columns follow each other, heads
+ * follow each other in a token's row: q is [num_tokens, heads_q * head_dim]
+ * with row stride ldq, k alike, both may be columns of one joint matrix. A
+ * kind with 0 heads has its pointers ignored.
+ */
+typedef struct lora_qk_heads_t {
+  int32_t heads_q;      /* 0..65536 */
+  int32_t heads_k;      /* 0..65536, not both 0 */
+  int32_t head_dim;     /* a multiple of 8, up to 256 */
+  int32_t rot_dim;      /* a multiple of 16 from 0 (no rotation) to head_dim */
+  int32_t neighbours;   /* 0: pairs (i, i + rot_dim / 2); otherwise (2 i, 2 i + 1) */
+  float eps;            /* > 0 */
+  const void* weight_q; /* DEVICE bf16 [head_dim], 16-byte aligned */
+  const void* weight_k;
+  const double* freqs;  /* DEVICE fp64 [rot_dim / 2], radians per position */
+} lora_qk_heads_t;
+
+/*
+ * positions: DEVICE int32 [num_tokens]. q_out / k_out may be q / k themselves
+ * (the same address and stride); otherwise the buffers must not overlap. Can
+ * be captured into a HIP graph.
+ */
+int lora_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, const lora_qk_heads_t* heads,
+                      const int32_t* positions, int32_t num_tokens, void* q_out, int64_t ldqo, void* k_out,
+                      int64_t ldko, void* stream);
+
+/*
+ * Its gradient: from the inputs q, k and the outputs' gradients dq_out, dk_out
+ * (bf16 rows like q_out, k_out), with m the gradient turned back and g = m w,
+ *     dx = r (g - x r mean(g x r))         as bf16 rows dq, dk,
+ *     dweight[0] = sum over tokens and query heads of m x r,  dweight[1] over
+ *     key heads: fp32 [2, head_dim]; NULL: not computed (frozen weights)
+ * With LORA_GRAD_ACCUMULATE dweight is added to, otherwise overwritten (with
+ * zeros for no tokens). The order of its sums is fixed: the same call gives
+ * the same bits. dweight needs a workspace of lora_workspace_size_qk() bytes,
+ * 16-byte aligned, in any state; calls that share one must be ordered. The
+ * buffers must not overlap. Can be captured into a HIP graph.
+ */
+int lora_workspace_size_qk(const lora_qk_heads_t* heads, int32_t num_tokens, size_t* bytes);
+int lora_qk_norm_rope_backward(const void* q, int64_t ldq, const void* k, int64_t ldk, const lora_qk_heads_t* heads,
+                               const int32_t* positions, int32_t num_tokens, const void* dq_out, int64_t lddqo,
+                               const void* dk_out, int64_t lddko, void* dq, int64_t lddq, void* dk, int64_t lddk,
+                               float* dweight, uint32_t flags, void* ws, size_t ws_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* lora_status_string(int status);
 

@@ -63,12 +63,19 @@ class CQ4(ctypes.Structure):
                 ("ld_exps", ctypes.c_int64), ("rows", ctypes.c_int32), ("width", ctypes.c_int32)]
 
 
+class CQKHeads(ctypes.Structure):
+    _fields_ = [("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("neighbours", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("weight_q", ctypes.c_void_p), ("weight_k", ctypes.c_void_p), ("freqs", ctypes.c_void_p)]
+
+
 EXPORTS = ["lora_segments_from_ids", "lora_workspace_size", "lora_sgmv_shrink", "lora_sgmv_expand",
            "lora_sgmv_fused", "lora_packed_backward", "lora_workspace_size_multi",
            "lora_sgmv_fused_multi", "lora_sgmv_fused_noalloc", "lora_workspace_size_graph",
            "lora_sgmv_fused_graph", "lora_q8_quantize", "lora_q8_dequantize", "lora_q8_matmul",
            "lora_packed_backward_q8", "lora_swiglu", "lora_swiglu_backward", "lora_q4_quantize", "lora_q4_dequantize",
-           "lora_q4_matmul", "lora_q4_matmul_q8", "lora_status_string", "lora_last_error", "lora_version"]
+           "lora_q4_matmul", "lora_q4_matmul_q8", "lora_qk_norm_rope", "lora_workspace_size_qk",
+           "lora_qk_norm_rope_backward", "lora_status_string", "lora_last_error", "lora_version"]
 NOALLOC_SCRATCH_BYTES = 16 << 20  # LORA_NOALLOC_SCRATCH_BYTES
 
 _lib = None
@@ -125,6 +132,11 @@ def load(path: str = LIB_PATH):
     lib.lora_q4_dequantize.argtypes = [P, P, I64, P]
     lib.lora_q4_matmul.argtypes = [P, P, P, I64, ctypes.c_uint32, P]
     lib.lora_q4_matmul_q8.argtypes = [Q, P, P, I64, ctypes.c_uint32, P]
+    I32 = ctypes.c_int32
+    lib.lora_qk_norm_rope.argtypes = [P, I64, P, I64, P, P, I32, P, I64, P, I64, P]  # (a CQKHeads by its address)
+    lib.lora_workspace_size_qk.argtypes = [P, I32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.lora_qk_norm_rope_backward.argtypes = [P, I64, P, I64, P, P, I32, P, I64, P, I64, P, I64, P, I64, P,
+                                               ctypes.c_uint32, P, ctypes.c_size_t, P]
     lib.lora_status_string.restype = ctypes.c_char_p
     lib.lora_status_string.argtypes = [ctypes.c_int]
     lib.lora_last_error.restype = ctypes.c_char_p
@@ -655,6 +667,91 @@ def q4_matmul(x, w: Q4, y, accumulate: bool = False, stream=None):
     fn = lib.lora_q4_matmul if isinstance(x, Q4) else lib.lora_q4_matmul_q8
     ldy = _rows_arg("y", y, x.rows, w.rows, dev)
     _call_on(dev, stream, fn, x.addr, _q8_arg("w", w, dev), y.data_ptr(), ldy, 1 if accumulate else 0)
+
+
+# ---------------------------------------------------------------------------
+# The norm and rotation of queries and keys
+# ---------------------------------------------------------------------------
+class QKHeads:
+    """The heads of the q and k projections: bf16 norm weights [head_dim] (None
+    where there are no heads of the kind) and float64 frequencies, in radians
+    per position, of the turned pairs (len(freqs) * 2 columns of each head)."""
+
+    def __init__(self, heads_q: int, heads_k: int, head_dim: int, weight_q, weight_k, freqs, eps: float = 1e-6,
+                 neighbours: bool = False):
+        import torch
+        self.heads_q, self.heads_k, self.head_dim = int(heads_q), int(heads_k), int(head_dim)
+        for name, t, n, dtype in (("weight_q", weight_q, self.head_dim if self.heads_q else 0, torch.bfloat16),
+                                  ("weight_k", weight_k, self.head_dim if self.heads_k else 0, torch.bfloat16),
+                                  ("freqs", freqs, None, torch.float64)):
+            if t is None and not n:
+                continue
+            if t is None or t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() or n and t.numel() != n:
+                raise ValueError(f"{name} must be a contiguous {dtype} vector" + (f" of {n}" if n else "")
+                                 + ("" if t is None else f", got {t.dtype} {tuple(t.shape)}"))
+        kept = [t for t in (weight_q, weight_k, freqs) if t is not None]
+        if len({t.device for t in kept}) != 1:
+            raise ValueError("weights and freqs must be on one device")
+        self.rot_dim = 2 * int(freqs.numel()) if freqs is not None else 0
+        self.weight_q, self.weight_k, self.freqs = weight_q, weight_k, freqs
+        self.dev = kept[0].get_device()
+        self._c = CQKHeads(self.heads_q, self.heads_k, self.head_dim, self.rot_dim, int(bool(neighbours)), float(eps),
+                           _ptr(weight_q), _ptr(weight_k), _ptr(freqs))
+        self.addr = ctypes.addressof(self._c)
+
+
+def _qk_rows(name: str, t, heads: int, rows: int, h: QKHeads):
+    """(address, row stride) of the rows of one kind of heads."""
+    if not heads:
+        return None, 0
+    if t is None:
+        raise ValueError(f"{name} is None, but there are {heads} heads of its kind")
+    return t.data_ptr(), _rows_arg(name, t, rows, heads * h.head_dim, h.dev)
+
+
+def _qk_positions(positions, dev: int) -> int:
+    if positions.dtype is not _torch.int32 or positions.dim() != 1 or not positions.is_contiguous() or positions.get_device() != dev:
+        raise ValueError(f"positions must be a contiguous int32 vector on {_dev_name(dev)}, got {positions.dtype} "
+                         f"{tuple(positions.shape)} on {positions.device}")
+    return positions.shape[0]
+
+
+def qk_norm_rope(q, k, heads: QKHeads, positions, q_out, k_out, stream=None):
+    """The norm of every head of q [T, heads_q * head_dim] and k, and its
+    rotation by positions [T], into q_out and k_out (which may be q and k)."""
+    lib, h = _lib or load(), heads
+    T = _qk_positions(positions, h.dev)
+    _call_on(h.dev, stream, lib.lora_qk_norm_rope, *_qk_rows("q", q, h.heads_q, T, h), *_qk_rows("k", k, h.heads_k, T, h),
+             h.addr, positions.data_ptr(), T, *_qk_rows("q_out", q_out, h.heads_q, T, h),
+             *_qk_rows("k_out", k_out, h.heads_k, T, h))
+
+
+def new_workspace_qk(heads: QKHeads, num_tokens: int):
+    """The workspace of qk_norm_rope_backward with dweight."""
+    import torch
+    lib = load()
+    n = ctypes.c_size_t(0)
+    _check(lib.lora_workspace_size_qk(heads.addr, int(num_tokens), ctypes.byref(n)))
+    return torch.empty(max(16, n.value), dtype=torch.uint8, device=f"cuda:{heads.dev}")
+
+
+def qk_norm_rope_backward(q, k, heads: QKHeads, positions, dq_out, dk_out, dq, dk, dweight=None, flags: int = 0,
+                          ws=None, stream=None):
+    """The gradient of qk_norm_rope: dq and dk from the outputs' gradients, and
+    with dweight (float32 [2, head_dim], needs ws) those of both weights."""
+    lib, h = _lib or load(), heads
+    T = _qk_positions(positions, h.dev)
+    if dweight is not None and (dweight.dtype is not _torch.float32 or tuple(dweight.shape) != (2, h.head_dim)
+                                or not dweight.is_contiguous() or dweight.get_device() != h.dev):
+        raise ValueError(f"dweight must be a contiguous float32 [2, {h.head_dim}] tensor on {_dev_name(h.dev)}")
+    if ws is not None and ws.get_device() != h.dev:
+        raise ValueError(f"ws is on {ws.device}, expected {_dev_name(h.dev)}")
+    wp, wb = _ws(ws)
+    _call_on(h.dev, stream, lib.lora_qk_norm_rope_backward, *_qk_rows("q", q, h.heads_q, T, h),
+             *_qk_rows("k", k, h.heads_k, T, h), h.addr, positions.data_ptr(), T,
+             *_qk_rows("dq_out", dq_out, h.heads_q, T, h), *_qk_rows("dk_out", dk_out, h.heads_k, T, h),
+             *_qk_rows("dq", dq, h.heads_q, T, h), *_qk_rows("dk", dk, h.heads_k, T, h),
+             _ptr(dweight), int(flags), wp, wb)
 
 
 class CPlanItem(ctypes.Structure):

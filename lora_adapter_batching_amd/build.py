@@ -13,7 +13,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblora_sgmv.so")
 SOURCES = ["lora_api.cpp", "lora_fwd.hip", "lora_bwd.hip", "lora_noalloc.hip",
-           "lora_q8.hip", "lora_q8_matmul.hip", "lora_q4.hip", "lora_q4_matmul.hip"]
+           "lora_q8.hip", "lora_q8_matmul.hip", "lora_q4.hip", "lora_q4_matmul.hip", "lora_qk.hip"]
 ARCH = os.environ.get("LORA_OFFLOAD_ARCH", "gfx950")
 
 
