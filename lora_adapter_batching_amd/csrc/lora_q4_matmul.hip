@@ -88,7 +88,7 @@ __device__ __forceinline__ void ring_barrier() {
   if constexpr (WAVES > 1) __builtin_amdgcn_s_barrier();
 }
 __device__ __forceinline__ i32x4 rsrc_words(uint64_t base, int32_t bytes) {
-  return i32x4{(int)(uint32_t)base, (int)((uint32_t)(base >> 32) & 0xffffu), bytes, kRsrcWord3};
+  return i32x4{(int)(uint32_t)base, (int)(uint32_t)(base >> 32), bytes, kRsrcWord3};  // (addresses have 48 bits)
 }
 
 // Tile of workgroup b: each XCD (b % 8) takes a contiguous run of the tiles,
@@ -129,31 +129,31 @@ struct Tile4 {
   static constexpr int TT = BT / WT, TN = BN / WN;      // a wave's tokens and columns
   static constexpr int FT = TT / 32, FN = TN / 32;      // its fragments
   static constexpr int xrow_bytes = X8 ? 128 : 64;
-  static constexpr int xoff = BN * 64, eoff = xoff + BT * xrow_bytes;
+  static constexpr int wpieces = BN / 16, pieces = wpieces + BT * xrow_bytes / 1024;  // 1 KB each
+  static constexpr int vloads = (pieces + waves - 1) / waves;                          // of a wave
+  static constexpr int xoff = BN * 64, eoff = vloads * waves * 1024;
   static constexpr int wslots = (BN + 63) / 64, xslots = X8 ? 0 : (BT + 63) / 64;  // exponent loads, 64 rows each
   static constexpr int eloads = (wslots + xslots + waves - 1) / waves;             // of a wave
   static constexpr int stage = eoff + eloads * waves * 256;
-  static constexpr int wloads = BN / 16 / waves, xloads = BT * xrow_bytes / 1024 / waves;
-  static constexpr int loads = wloads + xloads + eloads;  // per wave and step
+  static constexpr int loads = vloads + eloads;           // per wave and step
   static constexpr int ring = S * stage;                  // one group's stages
   static constexpr int x8off = KS * ring;
-  static constexpr int x8loads = X8 ? (BT + 4 * waves - 1) / (4 * waves) : 0;  // 256 bytes (4 rows) each, per wave
+  static constexpr int x8loads = X8 ? BT / (8 * waves) : 0;  // 256 bytes (8 rows) each, per wave
   static constexpr int x8grp = x8loads * waves * 256;   // one group's exponents of 8-bit rows
   static constexpr int eprow = TN * 4 + 16;             // epilogue row of one token (fp32, padded)
   static constexpr int parts = (KS - 1) * BT * BN * 4;  // the other groups' sums
   static constexpr int epi = parts + waves * 32 * eprow;
   static constexpr int used = x8off + KS * x8grp;
   static constexpr int lds = used > epi ? used : epi;
-  static_assert(BN % (16 * waves) == 0 && BT * xrow_bytes % (1024 * waves) == 0, "whole loads, none of two operands");
-  static_assert(!X8 || BT % (4 * waves) == 0, "whole exponent loads");
+  static_assert(!X8 || BT % (8 * waves) == 0, "whole exponent loads");
   static_assert(TT % 32 == 0 && TN % 32 == 0, "whole fragments");
   static_assert(S >= 2 && lds <= 160 * 1024 && (S - 1) * loads < 64, "fits the LDS and the load counter");
 };
 
-// Exponents of 8-bit rows in LDS: rows of 16 dwords of four blocks each, dword d of
-// row r at position d ^ (r / 4) % 16 (the bank of a wave's 32 rows then differs),
+// Exponents of 8-bit rows in LDS: rows of 8 dwords of four blocks each, dword d of
+// row r at position d ^ (r / 8) % 8 (the bank of a wave's 32 rows then differs),
 // refilled every kExpBlocks blocks (the first dword may begin up to three blocks earlier).
-constexpr int kExpBlocks = 60;
+constexpr int kExpBlocks = 28;
 
 template <class C, bool ADD>
 __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args a) {
@@ -171,54 +171,72 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
   const int t0 = tt * C::BT, n0 = tn * C::BN;
   const int vt = min(C::BT, a.T - t0), vn = min(C::BN, a.N - n0);  // valid rows of the tile
 
-  const uint64_t wbase = reinterpret_cast<uint64_t>(a.w) + (uint64_t)n0 * 64;
-  const uint64_t webase = reinterpret_cast<uint64_t>(a.we) + (uint64_t)n0 * 4;
-  const uint64_t xbase = reinterpret_cast<uint64_t>(a.x) + (uint64_t)t0 * (X8 ? (uint64_t)a.ldx : 64u);
-  const uint64_t xebase = reinterpret_cast<uint64_t>(a.xe) + (uint64_t)t0 * (X8 ? (uint64_t)a.ldxe : 4u);
-  const int32_t xbytes = X8 ? (int32_t)((int64_t)(vt - 1) * a.ldx + (int64_t)a.nkb * 128) : vt * 64;
-
-  // Load p of the wave takes piece p * waves + wave of an operand: 16 rows of 64
-  // bytes or 8 of 128.
-  uint32_t wv[C::wloads], xv[C::xloads], ev[C::eloads];
+  // Load p of the wave takes piece p * waves + wave of the stage: 16 rows of 64 bytes
+  // (w, then x) or 8 of 128; then loads of 64 rows' exponents. Pieces behind
+  // the last one are empty.
+  uint32_t vv[C::vloads], ev[C::eloads];
+  bool isx[C::vloads], none[C::vloads];
 #pragma unroll
-  for (int p = 0; p < C::wloads; ++p)
-    wv[p] = (uint32_t)((p * C::waves + wave) * 1024 + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16));
-#pragma unroll
-  for (int p = 0; p < C::xloads; ++p) {
-    if constexpr (X8) {
-      const int r = 8 * (p * C::waves + wave) + (lane >> 3);
-      xv[p] = (uint32_t)((int64_t)r * a.ldx) + 16u * ((lane & 7) ^ ((r >> 1) & 7));
-    } else {
-      xv[p] = (uint32_t)((p * C::waves + wave) * 1024 + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16));
-    }
-  }
-#pragma unroll
-  for (int p = 0; p < C::eloads; ++p) {
+  for (int p = 0; p < C::vloads; ++p) {
     const int q = p * C::waves + wave;
-    ev[p] = 4u * (uint32_t)(lane + 64 * (q >= C::wslots ? q - C::wslots : q));
+    isx[p] = p * C::waves >= C::wpieces || ((p + 1) * C::waves > C::wpieces && q >= C::wpieces);
+    none[p] = (p + 1) * C::waves > C::pieces && q >= C::pieces;
+    const int qx = isx[p] ? q - C::wpieces : q;
+    const uint32_t v4 = (uint32_t)(qx * 1024 + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16));
+    const int r = 8 * qx + (lane >> 3);
+    vv[p] = X8 && isx[p] ? (uint32_t)((int64_t)r * a.ldx) + 16u * ((lane & 7) ^ ((r >> 1) & 7)) : v4;
   }
   uint8_t* const ring = smem + grp * C::ring;
   const uint32_t ring0 = lds0 + (uint32_t)(grp * C::ring);
-  // Load p of panel kb; behind the group's last one the descriptors are empty and the
-  // loads write zeros, so that every step issues (and waits for) the same
+  // Where the loads stand: the next panel's addresses and stage. (Walked by
+  // scalar additions: the addresses made from the panel's number took 45 scalar
+  // instructions in one place of the step.)
+  struct {
+    uint64_t w, x, e[C::eloads], estep[C::eloads];
+    int32_t wbytes, xbytes, ebytes[C::eloads];
+    uint32_t xat, at;
+    int left;
+  } to;
+  to.w = reinterpret_cast<uint64_t>(a.w) + (uint64_t)n0 * 64 + (uint64_t)k0 * a.ldw;
+  to.wbytes = vn * 64;
+  const uint64_t xbase = reinterpret_cast<uint64_t>(a.x) + (uint64_t)t0 * (X8 ? (uint64_t)a.ldx : 64u);
+  const uint64_t xebase = reinterpret_cast<uint64_t>(a.xe) + (uint64_t)t0 * (X8 ? (uint64_t)a.ldxe : 4u);
+  to.x = X8 ? xbase : xbase + (uint64_t)k0 * a.ldx;
+  to.xbytes = X8 ? (int32_t)((int64_t)(vt - 1) * a.ldx + (int64_t)a.nkb * 128) : vt * 64;
+  to.xat = (uint32_t)k0 * 128u;
+#pragma unroll
+  for (int p = 0; p < C::eloads; ++p) {
+    const int q = p * C::waves + wave;
+    const bool isx = q >= C::wslots;
+    ev[p] = 4u * (uint32_t)(lane + 64 * (isx ? q - C::wslots : q));
+    to.estep[p] = (uint64_t)(isx ? a.ldxe : a.ldwe);
+    to.e[p] = (isx ? xebase : reinterpret_cast<uint64_t>(a.we) + (uint64_t)n0 * 4) + (uint64_t)k0 * to.estep[p];
+    to.ebytes[p] = (isx ? (X8 ? 0 : vt) : vn) * 4;
+  }
+  to.at = ring0;
+  to.left = k1 - k0;
+  // Load p of the panel; behind the group's last one the descriptors are empty and
+  // the loads write zeros, so that every step issues (and waits for) the same
   // number without a branch between them.
-  auto load = [&](int kb, int slot, int p) {
-    const bool live = kb < k1;
-    const uint32_t at = ring0 + (uint32_t)(slot * C::stage);
-    if (p < C::wloads) {
-      load_piece16(rsrc_words(wbase + (uint64_t)kb * a.ldw, live ? vn * 64 : 0), at + (p * C::waves + wave) * 1024, wv[p], 0);
-    } else if (p < C::wloads + C::xloads) {
-      const int q = p - C::wloads;
-      const uint32_t to = at + C::xoff + (q * C::waves + wave) * 1024;
-      if constexpr (X8) load_piece16(rsrc_words(xbase, live ? xbytes : 0), to, xv[q], (uint32_t)kb * 128u);
-      else load_piece16(rsrc_words(xbase + (uint64_t)kb * a.ldx, live ? xbytes : 0), to, xv[q], 0);
+  auto load = [&](int p) {
+    const bool live = to.left > 0;
+    if (p < C::vloads) {
+      const int32_t bytes = isx[p] ? to.xbytes : to.wbytes;
+      load_piece16(rsrc_words(isx[p] ? to.x : to.w, live && !none[p] ? bytes : 0), to.at + (p * C::waves + wave) * 1024, vv[p],
+                   X8 && isx[p] ? to.xat : 0);
     } else {
-      const int q = p - C::wloads - C::xloads, slotq = q * C::waves + wave;
-      const bool isx = slotq >= C::wslots;
-      const uint64_t base = isx ? xebase + (uint64_t)kb * a.ldxe : webase + (uint64_t)kb * a.ldwe;
-      const int rows = isx ? (X8 ? 0 : vt) : vn;
-      load_piece4(rsrc_words(base, live ? rows * 4 : 0), at + C::eoff + slotq * 256, ev[q]);
+      const int q = p - C::vloads;
+      load_piece4(rsrc_words(to.e[q], live ? to.ebytes[q] : 0), to.at + C::eoff + (q * C::waves + wave) * 256, ev[q]);
     }
+  };
+  auto next_panel = [&] {
+    to.w += (uint64_t)a.ldw;
+    if constexpr (X8) to.xat += 128u;
+    else to.x += (uint64_t)a.ldx;
+#pragma unroll
+    for (int p = 0; p < C::eloads; ++p) to.e[p] += to.estep[p];
+    to.at = to.at == ring0 + (C::S - 1) * C::stage ? ring0 : to.at + C::stage;
+    --to.left;
   };
   // 8-bit rows: the dwords with blocks kb0 .. of the group. What lies behind a
   // row's last block is never used.
@@ -229,8 +247,8 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
     const i32x4 xer = rsrc_words(xebase, (int32_t)((int64_t)(vt - 1) * a.ldxe + 4 * dwords));
 #pragma unroll
     for (int p = 0; p < C::x8loads; ++p) {
-      const int r0 = 4 * (p * C::waves + wave), r = r0 + (lane >> 4);
-      load_piece4(xer, xs0 + r0 * 64, (uint32_t)((int64_t)r * a.ldxe) + 4u * ((lane & 15) ^ ((r >> 2) & 15)) + (uint32_t)(kb0 & ~3));
+      const int r0 = 8 * (p * C::waves + wave), r = r0 + (lane >> 3);
+      load_piece4(xer, xs0 + r0 * 32, (uint32_t)((int64_t)r * a.ldxe) + 4u * ((lane & 7) ^ ((r >> 3) & 7)) + (uint32_t)(kb0 & ~3));
     }
   };
 
@@ -248,11 +266,11 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
   };
   const int p4 = (h ^ ((m >> 2) & 3)) * 16;
   const int p80 = (h ^ ((m >> 1) & 7)) * 16, p81 = ((2 + h) ^ ((m >> 1) & 7)) * 16;
-  auto read_w = [&](int slot, int s, int f) {
-    return frag4(*reinterpret_cast<const u32x4*>(ring + slot * C::stage + (wrow + 32 * f) * 64 + (p4 ^ (32 * s))));
+  auto read_w = [&](int at, int s, int f) {
+    return frag4(*reinterpret_cast<const u32x4*>(ring + at + (wrow + 32 * f) * 64 + (p4 ^ (32 * s))));
   };
-  auto read_x = [&](int slot, int s, int f) {
-    const uint8_t* p = ring + slot * C::stage + C::xoff + (xrow + 32 * f) * C::xrow_bytes;
+  auto read_x = [&](int at, int s, int f) {
+    const uint8_t* p = ring + at + C::xoff + (xrow + 32 * f) * C::xrow_bytes;
     if constexpr (X8)
       return frag8(*reinterpret_cast<const u32x4*>(p + (p80 ^ (64 * s))), *reinterpret_cast<const u32x4*>(p + (p81 ^ (64 * s))));
     else
@@ -260,15 +278,15 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
   };
   // The dwords that hold a step's exponents; shifted into place apart from the
   // read, which takes its time: bytes 0 and 2 are then a lane's own in the two halves.
-  auto read_exps = [&](int slot, int kb, int kb0, Exps& e) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(ring + slot * C::stage + C::eoff);
+  auto read_exps = [&](int at, int kb, int kb0, Exps& e) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(ring + at + C::eoff);
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) e.w[j] = (int)p[wrow + 32 * j];
 #pragma unroll
     for (int i = 0; i < C::FT; ++i) {
       if constexpr (X8) {
         const int d = (kb >> 2) - (kb0 >> 2), r = xrow + 32 * i;
-        e.x[i] = (int)xs[r * 16 + ((d ^ (r >> 2)) & 15)];
+        e.x[i] = (int)xs[r * 8 + ((d ^ (r >> 3)) & 7)];
       } else {
         e.x[i] = (int)p[64 * C::wslots + xrow + 32 * i];
       }
@@ -288,27 +306,32 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
     return o;
   };
   i32x8 fw[2][C::FN], fx[2][C::FT];
-  // Half s of the group's step i: multiplies fragment set s and reads set s ^ 1 (the next
-  // half). Half 1 issues the loads of step i + S into the stage of step i,
-  // which every wave has read by then.
-  auto half = [&](auto sc, const Exps& e, int i, int kb0, Exps& raw) {
+  // Half s of the group's step i, whose stage is at `at` (the next one's at `nx`):
+  // multiplies fragment set s and reads set s ^ 1 (the next half), early, so that
+  // nothing is outstanding where the waves meet. The stage of step i is read
+  // by then, and takes the panel of step i + S: the first loads in half 1, the
+  // others in half 0 of step i + 1.
+  constexpr int M = C::FT * C::FN, F = C::FN + C::FT;
+  constexpr int early = (F + (M > 1 ? M / 2 : 1) - 1) / (M > 1 ? M / 2 : 1);
+  constexpr int ahead = C::S == 2 ? C::loads : C::loads / 2;  // loads of half 1 (two stages: those of half 0 would be waited for at once)
+  auto half = [&](auto sc, const Exps& e, int at, int nx, int kb, int kb0, Exps& raw) {
     constexpr int s = decltype(sc)::value;
-    constexpr int M = C::FT * C::FN, F = C::FN + C::FT;
-    const int slot = (i + s) % C::S;
 #pragma unroll
     for (int n = 0; n < M; ++n) {
       const int t = n / C::FN, j = n % C::FN;
       acc[t][j] = mfma4_32<X8, s>(fw[s][j], fx[s][t], acc[t][j], e.w[j], e.x[t]);
 #pragma unroll
-      for (int f = n * F / M; f < (n + 1) * F / M; ++f) {
-        if (f < C::FN) fw[s ^ 1][f] = read_w(slot, s ^ 1, f);
-        else fx[s ^ 1][f - C::FN] = read_x(slot, s ^ 1, f - C::FN);
+      for (int f = n * early; f < (n + 1) * early && f < F; ++f) {
+        if (f < C::FN) fw[s ^ 1][f] = read_w(s ? nx : at, s ^ 1, f);
+        else fx[s ^ 1][f - C::FN] = read_x(s ? nx : at, s ^ 1, f - C::FN);
       }
-      if constexpr (s == 1) {
-        // (behind the last panel this reads a row that nothing uses)
-        if (n == M / 2) read_exps(slot, k0 + i + 1, kb0, raw);
+      // (behind the last panel this reads a row that nothing uses)
+      if (s == 1 && n == M / 2) read_exps(nx, kb + 1, kb0, raw);
+      if (n >= M / 2) {
+        constexpr int R = M - M / 2, first = s ? 0 : ahead, count = s ? ahead : C::loads - ahead;
+        const int q = n - M / 2;
 #pragma unroll
-        for (int p = n * C::loads / M; p < (n + 1) * C::loads / M; ++p) load(k0 + i + C::S, i % C::S, p);
+        for (int p = first + q * count / R; p < first + (q + 1) * count / R; ++p) load(p);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -316,10 +339,12 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
 
   if constexpr (X8) load_exps(k0);
 #pragma unroll
-  for (int s = 0; s < C::S; ++s)
+  for (int s = 0; s < C::S; ++s) {
 #pragma unroll
-    for (int p = 0; p < C::loads; ++p) load(k0 + s, s, p);
-  wait_vm<(C::S - 1) * C::loads>();
+    for (int p = 0; p < (s < C::S - 1 ? C::loads : ahead); ++p) load(p);
+    if (s < C::S - 1) next_panel();
+  }
+  wait_vm<(C::S - 2) * C::loads + ahead>();
   wait_lds();
   ring_barrier<C::waves>();
 #pragma unroll
@@ -327,6 +352,7 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
 #pragma unroll
   for (int i = 0; i < C::FT; ++i) fx[0][i] = read_x(0, 0, i);
   const int span = X8 ? kExpBlocks : steps;
+  int at = 0;
   for (int i0 = 0; i0 < steps; i0 += span) {
     const int kb0 = k0 + i0;
     if (X8 && i0) {
@@ -335,19 +361,22 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
       ring_barrier<C::waves>();
     }
     Exps raw;
-    read_exps(i0 % C::S, kb0, kb0, raw);
+    read_exps(at, kb0, kb0, raw);
     Exps e = shift_exps(kb0, raw);
     const int i1 = min(steps, i0 + span);
     for (int i = i0; i < i1; ++i) {
-      half(std::integral_constant<int, 0>{}, e, i, kb0, raw);
+      const int nx = at == (C::S - 1) * C::stage ? 0 : at + C::stage;
+      half(std::integral_constant<int, 0>{}, e, at, nx, k0 + i, kb0, raw);
+      next_panel();
       // step i is in registers; step i + 1 has landed (the later ones may still
       // be in flight); the barrier makes both true for every wave
       wait_vm<(C::S - 2) * C::loads>();
       wait_lds();
       ring_barrier<C::waves>();
       __builtin_amdgcn_sched_barrier(0);
-      half(std::integral_constant<int, 1>{}, e, i, kb0, raw);
+      half(std::integral_constant<int, 1>{}, e, at, nx, k0 + i, kb0, raw);
       e = shift_exps(k0 + i + 1, raw);
+      at = nx;
     }
     // the exponents are refilled only when every wave has read its last ones
     wait_lds();
@@ -525,7 +554,22 @@ void launch_few(const Mat4Args& a, bool add, hipStream_t s) {
 
 // Tiles to choose from. A workgroup of a tile takes about fixed + step * (its
 // panels of the sum) microseconds while `slots` of them run, so a product takes
-// that times the rounds its tiles need.
+// that times the rounds its tiles need: a fit to these times on 256 CUs (us; tiles
+// by tokens x columns, / the groups that share the sum; 8-bit x, then 4-bit x).
+//   tokens, k, n        256x256    256x128    128x160    128x128     128x96      64x64    64x96/2    64x64/4    32x64/4    32x32/4
+//   37, 2560, 2560                                                           7.1   5.8  7.1   6.4  6.6   5.5  5.0   4.5  4.4   3.9
+//   37, 9728, 2560                                                          20.1  15.2 16.1  14.6 13.0  10.2  9.9   8.7  8.0   6.5
+//   100, 9728, 2560                                                         20.1  15.3 16.7  14.7 13.6  10.3 10.2   8.8 14.0   9.2
+//   128, 2560, 19456                         12.5  11.1 11.4  9.8 10.4  9.4 15.1  10.4 14.7  10.6
+//   256, 9728, 2560                                                         20.2  15.4 17.0  14.9 14.2  10.9 19.4  13.6 20.9  14.3
+//   256, 2560, 19456              17.5 13.2  14.7  12.7 18.0 13.5 18.0 13.5 21   16    24    17
+//   512, 2560, 2560                                     10.7  9.0 10.0  9.0  9.0   7.7  7.9   7.0 11.9   7.9
+//   512, 4096, 14336              27.0 21.5  34.5  29   28   22   39   28
+//   2048, 4096, 4096              28.5 22.1  34.9  25.5 29.1 24.1 35.4 25.5
+//   8191, 4096, 4096   94   69   117   75   138    94   115   80
+//   8192, 4096, 14336  324  236  398  249   454   320   386  276
+// Over the 34 products measured for it the choice is the fastest tile of the list or within
+// 7% of it. Nothing in the fit stands for the weights' bytes.
 struct TileChoice {
   int bt, bn, ks, stages, slots;
   float fixed, step;
@@ -536,18 +580,28 @@ constexpr TileChoice choice(int slots, float fixed, float step) {
   return TileChoice{C::BT, C::BN, C::KS, C::S, slots, fixed, step, launch_tile<C>};
 }
 const TileChoice kTiles8[] = {
-    choice<Tile4<256, 256, 2, 2, 2, true, 1, true>>(256, 10.6f, 1.40f),
-    choice<Tile4<128, 128, 2, 2, 3, true>>(256, 6.2f, 0.34f),
-    choice<Tile4<128, 64, 2, 2, 3, true>>(256, 4.9f, 0.26f),
-    choice<Tile4<32, 64, 1, 2, 3, true, 4>>(256, 3.4f, 0.56f),
-    choice<Tile4<32, 32, 1, 1, 4, true, 4>>(256, 3.1f, 0.39f),
+    choice<Tile4<256, 256, 2, 2, 3, true, 1, true>>(256, 6.5f, 1.05f),
+    choice<Tile4<256, 128, 4, 1, 3, true>>(256, 5.2f, 0.62f),
+    choice<Tile4<128, 160, 4, 1, 3, true>>(256, 5.0f, 0.39f),
+    choice<Tile4<128, 128, 2, 2, 3, true>>(256, 3.6f, 0.34f),
+    choice<Tile4<128, 96, 4, 1, 4, true>>(256, 4.0f, 0.30f),
+    choice<Tile4<64, 64, 2, 2, 4, true>>(512, 3.2f, 0.23f),
+    choice<Tile4<64, 96, 2, 1, 3, true, 2>>(256, 4.1f, 0.32f),
+    choice<Tile4<64, 64, 2, 1, 3, true, 4>>(256, 4.0f, 0.50f),
+    choice<Tile4<32, 64, 1, 2, 3, true, 4>>(256, 2.8f, 0.38f),
+    choice<Tile4<32, 32, 1, 1, 4, true, 4>>(256, 2.3f, 0.27f),
 };
 const TileChoice kTiles4[] = {
-    choice<Tile4<256, 256, 2, 2, 4, false, 1, true>>(256, 10.6f, 0.70f),
-    choice<Tile4<128, 128, 2, 2, 3, false>>(256, 6.2f, 0.24f),
-    choice<Tile4<128, 64, 2, 2, 3, false>>(256, 4.9f, 0.20f),
-    choice<Tile4<32, 64, 1, 2, 3, false, 4>>(256, 3.4f, 0.40f),
-    choice<Tile4<32, 32, 1, 1, 4, false, 4>>(256, 3.1f, 0.39f),
+    choice<Tile4<256, 256, 2, 2, 3, false, 1, true>>(256, 6.2f, 0.66f),
+    choice<Tile4<256, 128, 4, 1, 3, false>>(256, 4.8f, 0.41f),
+    choice<Tile4<128, 160, 4, 1, 3, false>>(256, 4.7f, 0.32f),
+    choice<Tile4<128, 128, 2, 2, 3, false>>(256, 2.8f, 0.27f),
+    choice<Tile4<128, 96, 4, 1, 4, false>>(256, 3.1f, 0.23f),
+    choice<Tile4<64, 64, 2, 2, 4, false>>(512, 2.7f, 0.17f),
+    choice<Tile4<64, 96, 2, 1, 3, false, 2>>(256, 2.8f, 0.30f),
+    choice<Tile4<64, 64, 2, 1, 3, false, 4>>(256, 3.6f, 0.36f),
+    choice<Tile4<32, 64, 1, 2, 3, false, 4>>(256, 1.6f, 0.33f),
+    choice<Tile4<32, 32, 1, 1, 4, false, 4>>(256, 1.2f, 0.20f),
 };
 constexpr int kTileCount = (int)(sizeof(kTiles8) / sizeof(kTiles8[0]));
 static_assert(sizeof(kTiles8) == sizeof(kTiles4), "as many of each");
@@ -556,8 +610,21 @@ constexpr int64_t kMaxTiles = 0xffffffffll / 512;
 
 // The tile for T tokens, N columns and a sum of nkb panels; null: the few-token kernel.
 const TileChoice* choose(bool x8, int32_t T, int32_t N, int32_t nkb) {
-  // (A launch holds fewer than 2^32 threads, 512 of them per workgroup.)
-  if (T <= kFewTokens && N <= 1 << 26) return nullptr;
+  // Up to one matrix fragment of tokens the weights' bytes are all that counts, as
+  // long as x is small: every 16 columns read all of it again. us, few-token kernel
+  // and the fastest tile:
+  //   tokens, k, n        8-bit x       4-bit x     x read, MB
+  //   1, 2560, 2560      2.8   4.2     2.8   3.8       0.4
+  //   1, 2560, 19456     6.4   7.6     6.7   7.1         3
+  //   1, 9728, 2560      5.8   7.0     5.8   6.3       1.6
+  //   16, 2560, 2560     3.7   4.3     2.9   3.8         7
+  //   16, 9728, 2560     8.1   7.2     5.9   6.3        25
+  //   16, 2560, 19456   10.1   8.0     6.6   7.4        50
+  //   16, 4096, 14336   14.8   8.4     7.6   8.0        59
+  // (MB of 8-bit x, half as many of 4-bit x.) The border of 32 MB is wrong for the
+  // fifth line alone. (A launch holds fewer than 2^32 threads, 512 of them per workgroup.)
+  const int64_t again = (int64_t)T * nkb * (x8 ? 128 : 64) * ((N + 15) / 16);
+  if (T <= kFewTokens && N <= 1 << 26 && again <= 32 << 20) return nullptr;
   const TileChoice* const all = x8 ? kTiles8 : kTiles4;
   const TileChoice* best = &all[0];  // (its grid is checked by the caller)
   double least = 0.;

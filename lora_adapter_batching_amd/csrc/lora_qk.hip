@@ -10,11 +10,16 @@
 //   dw += m x r,   dx = r (g - x r mean(g x r)).
 //
 // One pass over the data: the floor is the bytes. 8 columns of a head are one
-// lane's 16 bytes and a head is 4 to 32 neighbouring lanes, so a wave holds 2
-// to 16 heads of one token; the sums over a head stay in registers.
+// lane's 16 bytes and a head is 4 to 32 neighbouring lanes, so a wave holds a
+// group of 2 to 16 heads of one token; the sums over a head stay in registers. The
+// cosines and sines of a token are the same for all its heads: a workgroup
+// makes them once, one pair a thread, and its waves read them from LDS.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "lora_internal.h"
 #include "lora_q8.h"
@@ -26,19 +31,19 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
 struct QKArgs {
-  const uint16_t *q, *k;
-  int64_t ldq, ldk;
-  const uint16_t *gq, *gk;  // backward: the outputs' gradients
-  int64_t ldgq, ldgk;
-  uint16_t *oq, *ok;        // outputs, or the inputs' gradients
-  int64_t ldoq, ldok;
-  const uint16_t *wq, *wk;
+  const uint16_t* x[2];     // rows of the queries and of the keys
+  int64_t ldx[2];
+  const uint16_t* g[2];     // backward: the outputs' gradients
+  int64_t ldg[2];
+  uint16_t* o[2];           // outputs, or the inputs' gradients
+  int64_t ldo[2];
+  const uint16_t* w[2];
   const double* freqs;
   const int32_t* positions;
   float* parts;             // backward: the workgroups' shares of dweight, or null
-  int32_t tokens, heads_q, heads, dim, rot;
-  int32_t per_token;        // items of one token
-  float eps;
+  int32_t heads[2];
+  int32_t tokens, dim, rot;
+  float eps, mean;          // mean = 1 / dim
 };
 
 // Sum over the L lanes of a head, in each of them.
@@ -56,47 +61,24 @@ __device__ __forceinline__ float sum_over(float v) {
   return v;
 }
 
-// What a lane needs of its token's rotation. The angle is taken in 64 bits and
-// reduced to part of a turn before it is rounded: position 131071 times a
-// frequency near 1 has no bits of the turn left in 32.
-template <bool NB>
-struct Turn {
-  static constexpr int N = NB ? 4 : 8;  // a lane's pairs
-  float c[N], s[N];
-  __device__ __forceinline__ void set(const QKArgs& a, int position, int chunk) {
-    const int half = a.rot >> 1;
-    const bool in = 8 * chunk < a.rot;
-    const int first = NB ? 4 * chunk : (8 * chunk < half ? 8 * chunk : 8 * chunk - half);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      c[i] = 1.f;
-      s[i] = 0.f;
-      if (in) {
-        const double t = (double)position * (a.freqs[first + i] * 0.15915494309189533577);
-        const float half_turns = (float)(2. * (t - __builtin_rint(t)));
-        sincospif(half_turns, &s[i], &c[i]);
-      }
-    }
-  }
+// cos and sin of the pairs of W tokens.
+constexpr int kMostPairs = 128;
+template <int W>
+struct Turns {
+  alignas(16) float c[W][kMostPairs], s[W][kMostPairs];
 };
-
-// The rotation of a lane's 8 columns (BACK: the other way). halves: `other` is the
-// pair's other member, from the lane that holds it; `upper` lanes hold the
-// second members.
-template <bool NB, bool BACK>
-__device__ __forceinline__ void turn8(float (&v)[8], const float (&other)[8], const Turn<NB>& t, bool upper) {
-  if constexpr (NB) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = v[2 * i], y = v[2 * i + 1], s = BACK ? -t.s[i] : t.s[i];
-      v[2 * i] = x * t.c[i] - y * s;
-      v[2 * i + 1] = y * t.c[i] + x * s;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float s = (upper != BACK) ? t.s[i] : -t.s[i];
-      v[i] = v[i] * t.c[i] + other[i] * s;
+// Fills it for tokens token0 ..; the caller synchronises. The angle is taken in 64
+// bits and reduced to part of a turn before it is rounded: position 131071 times
+// a frequency near 1 has few bits of the turn left in 32.
+template <int W>
+__device__ __forceinline__ void make_turns(const QKArgs& a, int token0, Turns<W>& t) {
+  const int half = a.rot >> 1;
+  for (int i = threadIdx.x; i < W * half; i += kThreads) {
+    const int k = i / half, pair = i - k * half;
+    if (token0 + k < a.tokens) {
+      const double turns = (double)a.positions[token0 + k] * (a.freqs[pair] * 0.15915494309189533577);
+      const float half_turns = (float)(2. * (turns - __builtin_rint(turns)));
+      sincospif(half_turns, &t.s[k][pair], &t.c[k][pair]);
     }
   }
 }
@@ -109,20 +91,47 @@ __device__ __forceinline__ u32x4 from_lane(u32x4 v, int lane) {
   return o;
 }
 
-// A lane's place: its chunk of the head, the lane that holds the other members of its
-// pairs, and its share of the wave's items.
+// A lane's place in its group of heads: its chunk of 8 columns, its head, and the
+// lane with the other members of its pairs (itself, where they are its own).
 template <int L, bool NB>
 struct Lane {
-  int chunk, head0, other;
-  bool in, upper;
+  int chunk, head, other;
+  bool in, turned, upper;
   __device__ __forceinline__ explicit Lane(const QKArgs& a) {
     const int lane = threadIdx.x & 63;
     chunk = lane & (L - 1);
-    head0 = lane / L;
+    head = lane / L;
     in = 8 * chunk < a.dim;
+    turned = 8 * chunk < a.rot;
     const int h = a.rot >> 4;  // chunks of half the turned columns
     upper = chunk >= h;
-    other = NB || 8 * chunk >= a.rot ? lane : upper ? lane - h : lane + h;
+    other = NB || !turned ? lane : upper ? lane - h : lane + h;
+  }
+  // The rotation of its columns: column e becomes c[e] times itself plus s[e] times
+  // its pair's other member.
+  template <int W>
+  __device__ __forceinline__ void turn(const QKArgs& a, const Turns<W>& t, int k, float (&c)[8], float (&s)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = 0.f;
+    if (!turned) return;
+    if constexpr (NB) {
+      const f32x4 vc = *reinterpret_cast<const f32x4*>(&t.c[k][4 * chunk]), vs = *reinterpret_cast<const f32x4*>(&t.s[k][4 * chunk]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = vc[e >> 1], s[e] = e & 1 ? vs[e >> 1] : -vs[e >> 1];
+    } else {
+      const int first = 8 * chunk - (upper ? a.rot >> 1 : 0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = t.c[k][first + e], s[e] = upper ? t.s[k][first + e] : -t.s[k][first + e];
+    }
+  }
+  // The other members of its pairs.
+  __device__ __forceinline__ void pairs(u32x4 v, const float (&f)[8], float (&p)[8]) const {
+    if constexpr (NB) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = f[e ^ 1];
+    } else {
+      unpack8(from_lane(v, other), p);
+    }
   }
 };
 
@@ -130,153 +139,172 @@ struct Lane {
 __device__ __forceinline__ bool past_range(float ss) { return !(ss < __builtin_inff()); }
 constexpr float kDown = 0x1p-80f;
 
-// U groups of 64 / L heads of one token per wave, all loaded before the first is
-// used.
-template <int L, bool NB, int U>
+// A workgroup takes W tokens: one for each wave (W = 4), or one whose groups of heads
+// the waves take in turn. U groups are loaded before the first is used.
+template <int L, bool NB, int W, int U>
 __global__ __launch_bounds__(kThreads) void qk_forward_kernel(QKArgs a) {
-  constexpr int H = 64 / L;  // heads a wave holds at once
-  const int item = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int token = item / a.per_token, part = item - token * a.per_token;
-  if (token >= a.tokens) return;
+  constexpr int H = 64 / L, STEP = W > 1 ? 1 : kWaves;
+  __shared__ Turns<W> turns;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int k = W > 1 ? wave : 0, g0 = W > 1 ? 0 : wave;
+  const int token = blockIdx.x * W + k;
+  const bool there = token < a.tokens;
   const Lane<L, NB> me(a);
-  u32x4 x[U];
-  bool live[U], key[U];
+  auto load = [&](int kind, int g) {
+    const int head = g * H + me.head;
+    if (!there || !me.in || head >= a.heads[kind]) return zero16();
+    return ld16(a.x[kind] + (int64_t)token * a.ldx[kind] + (int64_t)head * a.dim + 8 * me.chunk);
+  };
+  u32x4 x[2][U], w[2];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int head = (part * U + u) * H + me.head0;
-    key[u] = head >= a.heads_q;
-    live[u] = me.in && head < a.heads;
-    x[u] = zero16();
-    if (live[u]) {
-      const uint16_t* row = key[u] ? a.k + (int64_t)token * a.ldk + (int64_t)(head - a.heads_q) * a.dim
-                                   : a.q + (int64_t)token * a.ldq + (int64_t)head * a.dim;
-      x[u] = ld16(row + 8 * me.chunk);
-    }
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[i][u] = load(i, g0 + STEP * u);
+    w[i] = me.in && a.heads[i] ? ld16(a.w[i] + 8 * me.chunk) : zero16();
   }
-  u32x4 wq = zero16(), wk = zero16();
-  if (me.in && a.heads_q > 0) wq = ld16(a.wq + 8 * me.chunk);
-  if (me.in && a.heads > a.heads_q) wk = ld16(a.wk + 8 * me.chunk);
-  const u32x4 oq = from_lane(wq, me.other), ok = from_lane(wk, me.other);
-  Turn<NB> t;
-  t.set(a, a.positions[token], me.chunk);
+  make_turns(a, blockIdx.x * W, turns);
+  __syncthreads();
+  if (!there) return;
+  float c[8], s[8];
+  me.turn(a, turns, k, c, s);
+  auto heads_of = [&](auto kind_) {
+    constexpr int kind = decltype(kind_)::value;
+    // The weight goes into the rotation: column e of the output is
+    // r (A[e] x[e] + B[e] x[its pair's other]).
+    float A[8], B[8];
+    unpack8(w[kind], A);
+    me.pairs(w[kind], A, B);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float f[8], w[8], p[8], pw[8];
-    unpack8(x[u], f);
-    unpack8(key[u] ? wk : wq, w);
-    float ss = 0.f;
+    for (int e = 0; e < 8; ++e) A[e] *= c[e], B[e] *= s[e];
+    for (int g = g0; g * H < a.heads[kind]; g += STEP * U) {
+      u32x4 next[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += f[i] * f[i];
-    ss = sum_over<L>(ss);
-    float down = 1.f;
-    if (__any(past_range(ss))) {
-      down = past_range(ss) ? kDown : 1.f;
-      ss = 0.f;
+      for (int u = 0; u < U; ++u) next[u] = load(kind, g + STEP * (U + u));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += (f[i] * down) * (f[i] * down);
-      ss = sum_over<L>(ss);
+      for (int u = 0; u < U; ++u) {
+        float f[8], p[8];
+        unpack8(x[kind][u], f);
+        me.pairs(x[kind][u], f, p);
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
+        ss = sum_over<L>(ss);
+        float down = 1.f;
+        if (__any(past_range(ss))) {
+          down = past_range(ss) ? kDown : 1.f;
+          ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= down, p[e] *= down, ss += f[e] * f[e];
+          ss = sum_over<L>(ss);
+        }
+        const float r = __builtin_amdgcn_rsqf(ss * a.mean + a.eps * down * down);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = r * (f[e] * A[e] + p[e] * B[e]);
+        const int head = (g + STEP * u) * H + me.head;
+        if (me.in && head < a.heads[kind])
+          st16(a.o[kind] + (int64_t)token * a.ldo[kind] + (int64_t)head * a.dim + 8 * me.chunk, pack8(f));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[kind][u] = next[u];
     }
-    const float r = down * __builtin_amdgcn_rsqf(ss / (float)a.dim + a.eps * down * down);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
-    if constexpr (!NB) {
-      unpack8(from_lane(x[u], me.other), p);
-      unpack8(key[u] ? ok : oq, pw);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = me.other == (int)(threadIdx.x & 63) ? 0.f : p[i] * r * pw[i];
-    }
-    turn8<NB, false>(f, p, t, me.upper);
-    if (live[u]) {
-      const int head = (part * U + u) * H + me.head0;
-      uint16_t* row = key[u] ? a.ok + (int64_t)token * a.ldok + (int64_t)(head - a.heads_q) * a.dim
-                             : a.oq + (int64_t)token * a.ldoq + (int64_t)head * a.dim;
-      st16(row + 8 * me.chunk, pack8(f));
-    }
-  }
+  };
+  heads_of(std::integral_constant<int, 0>{});
+  heads_of(std::integral_constant<int, 1>{});
 }
 
-// One group of 64 / L heads per item; the waves of the grid take the items in
-// turn, so that a lane's share of dweight is summed over its items before it
-// meets the others' (in a fixed order: lanes, waves, then workgroups).
-template <int L, bool NB, bool DW>
+// The gradient. The grid is bounded and its workgroups take the tokens in turn, so
+// that a lane's share of dweight is summed over its tokens before it meets the
+// others' (in a fixed order: lanes, waves, then workgroups). The turns of a
+// workgroup's next tokens are made in the LDS half that the current ones leave.
+template <int L, bool NB, int W, bool DW>
 __global__ __launch_bounds__(kThreads) void qk_backward_kernel(QKArgs a) {
-  constexpr int H = 64 / L;
+  constexpr int H = 64 / L, STEP = W > 1 ? 1 : kWaves;
+  __shared__ Turns<W> turns[2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int k = W > 1 ? wave : 0, g0 = W > 1 ? 0 : wave;
   const Lane<L, NB> me(a);
-  u32x4 wq = zero16(), wk = zero16();
-  if (me.in && a.heads_q > 0) wq = ld16(a.wq + 8 * me.chunk);
-  if (me.in && a.heads > a.heads_q) wk = ld16(a.wk + 8 * me.chunk);
-  float dwq[8], dwk[8];
+  u32x4 w[2];
+  float dw[2][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
-  for (int token = blockIdx.x * kWaves + wave; token < a.tokens; token += gridDim.x * kWaves) {
-    Turn<NB> t;
-    t.set(a, a.positions[token], me.chunk);
-    for (int part = 0; part < a.per_token; ++part) {
-      const int head = part * H + me.head0;
-      const bool key = head >= a.heads_q, live = me.in && head < a.heads;
-      const int kh = head - a.heads_q;
-      u32x4 x = zero16(), g = zero16();
-      if (live) {
-        x = ld16((key ? a.k + (int64_t)token * a.ldk + (int64_t)kh * a.dim : a.q + (int64_t)token * a.ldq + (int64_t)head * a.dim) + 8 * me.chunk);
-        g = ld16((key ? a.gk + (int64_t)token * a.ldgk + (int64_t)kh * a.dim : a.gq + (int64_t)token * a.ldgq + (int64_t)head * a.dim) + 8 * me.chunk);
-      }
-      float f[8], m[8], p[8], w[8];
-      unpack8(x, f);
-      unpack8(g, m);
-      unpack8(key ? wk : wq, w);
-      if constexpr (!NB) {
-        unpack8(from_lane(g, me.other), p);
+  for (int i = 0; i < 2; ++i) {
+    w[i] = me.in && a.heads[i] ? ld16(a.w[i] + 8 * me.chunk) : zero16();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = me.other == (int)(threadIdx.x & 63) ? 0.f : p[i];
-      }
-      turn8<NB, true>(m, p, t, me.upper);
-      float ss = 0.f;
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+  }
+  int buf = 0;
+  for (int token0 = blockIdx.x * W; token0 < a.tokens; token0 += gridDim.x * W, buf ^= 1) {
+    const int token = token0 + k;
+    const bool there = token < a.tokens;
+    auto load = [&](int kind, int g, u32x4& x, u32x4& d) {
+      const int head = g * H + me.head;
+      x = d = zero16();
+      if (!there || !me.in || head >= a.heads[kind]) return;
+      x = ld16(a.x[kind] + (int64_t)token * a.ldx[kind] + (int64_t)head * a.dim + 8 * me.chunk);
+      d = ld16(a.g[kind] + (int64_t)token * a.ldg[kind] + (int64_t)head * a.dim + 8 * me.chunk);
+    };
+    u32x4 x[2], d[2];
+    load(0, g0, x[0], d[0]);
+    load(1, g0, x[1], d[1]);
+    make_turns(a, token0, turns[buf]);
+    __syncthreads();
+    if (!there) continue;
+    float c[8], s[8];
+    me.turn(a, turns[buf], k, c, s);
+    auto heads_of = [&](auto kind_) {
+      constexpr int kind = decltype(kind_)::value;
+      for (int g = g0; g * H < a.heads[kind]; g += STEP) {
+        u32x4 nx, nd;
+        load(kind, g + STEP, nx, nd);
+        float f[8], m[8], p[8], wf[8];
+        unpack8(x[kind], f);
+        unpack8(d[kind], m);
+        unpack8(w[kind], wf);
+        me.pairs(d[kind], m, p);
+        float ss = 0.f, along = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += f[i] * f[i];
-      ss = sum_over<L>(ss);
-      float down = 1.f;
-      if (__any(past_range(ss))) {
-        down = past_range(ss) ? kDown : 1.f;
-        ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= down, ss += f[i] * f[i];
+        for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
         ss = sum_over<L>(ss);
-      }
-      const float r = __builtin_amdgcn_rsqf(ss / (float)a.dim + a.eps * down * down);
-      float along = 0.f;
+        float down = 1.f;
+        if (__any(past_range(ss))) {
+          down = past_range(ss) ? kDown : 1.f;
+          ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f[i] *= r;  // x / rms
-        if constexpr (DW) {
-          dwq[i] += key ? 0.f : m[i] * f[i];
-          dwk[i] += key ? m[i] * f[i] : 0.f;
+          for (int e = 0; e < 8; ++e) f[e] *= down, ss += f[e] * f[e];
+          ss = sum_over<L>(ss);
         }
-        m[i] *= w[i];
-        along += m[i] * f[i];
-      }
-      along = sum_over<L>(along) / (float)a.dim;
+        const float r = __builtin_amdgcn_rsqf(ss * a.mean + a.eps * down * down);
+        float mw[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m[i] = (m[i] - f[i] * along) * r * down;
-      if (live)
-        st16((key ? a.ok + (int64_t)token * a.ldok + (int64_t)kh * a.dim : a.oq + (int64_t)token * a.ldoq + (int64_t)head * a.dim) + 8 * me.chunk,
-             pack8(m));
-    }
+        for (int e = 0; e < 8; ++e) {
+          mw[e] = m[e] * c[e] - p[e] * s[e];  // turned back
+          f[e] *= r;                          // x / rms
+          if constexpr (DW) dw[kind][e] += mw[e] * f[e];
+          mw[e] *= wf[e];
+          along += mw[e] * f[e];
+        }
+        along = sum_over<L>(along) * a.mean;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mw[e] = (mw[e] - f[e] * along) * r * down;
+        const int head = g * H + me.head;
+        if (me.in && head < a.heads[kind])
+          st16(a.o[kind] + (int64_t)token * a.ldo[kind] + (int64_t)head * a.dim + 8 * me.chunk, pack8(mw));
+        x[kind] = nx;
+        d[kind] = nd;
+      }
+    };
+    heads_of(std::integral_constant<int, 0>{});
+    heads_of(std::integral_constant<int, 1>{});
   }
   if constexpr (DW) {
     __shared__ float sum[kWaves][2][8 * L];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int d = L; d < 64; d *= 2) {
-        dwq[i] += __shfl_xor(dwq[i], d);
-        dwk[i] += __shfl_xor(dwk[i], d);
+      for (int e = 0; e < 8; ++e) {
+#pragma unroll
+        for (int l = L; l < 64; l *= 2) dw[i][e] += __shfl_xor(dw[i][e], l);
+        if (me.head == 0) sum[wave][i][8 * me.chunk + e] = dw[i][e];
       }
-      if (me.head0 == 0) {
-        sum[wave][0][8 * me.chunk + i] = dwq[i];
-        sum[wave][1][8 * me.chunk + i] = dwk[i];
-      }
-    }
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * a.dim; c += kThreads) {
       const int which = c >= a.dim, col = c - which * a.dim;
@@ -286,43 +314,58 @@ __global__ __launch_bounds__(kThreads) void qk_backward_kernel(QKArgs a) {
   }
 }
 
-// dweight = the workgroups' shares, 16 columns a workgroup: 16 threads take every
-// sixteenth share of a column, and their sums are added in order.
-__global__ __launch_bounds__(256) void qk_weight_kernel(const float* parts, int32_t n, int32_t cols, float* out, int32_t accumulate) {
-  __shared__ float sum[16][16 + 1];
+// dweight = the workgroups' shares, 16 columns a workgroup: 64 threads take every
+// 64th share of a column, and their sums are added in order.
+__global__ __launch_bounds__(1024) void qk_weight_kernel(const float* parts, int32_t n, int32_t cols, float* out, int32_t accumulate) {
+  __shared__ float sum[64][16 + 1];
   const int c = threadIdx.x & 15, r = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
   float s = 0.f;
-  if (col < cols)
-    for (int i = r; i < n; i += 16) s += parts[(int64_t)i * cols + col];
+  if (col < cols) {
+#pragma unroll 4
+    for (int i = r; i < n; i += 64) s += parts[(int64_t)i * cols + col];
+  }
   sum[r][c] = s;
   __syncthreads();
-  if (r == 0 && col < cols) {
+  if (r < 4) {
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += sum[i][c];
+    for (int i = 0; i < 16; ++i) s += sum[16 * r + i][c];
+  }
+  __syncthreads();
+  if (r < 4) sum[r][c] = s;
+  __syncthreads();
+  if (r == 0 && col < cols) {
+    s = (sum[0][c] + sum[1][c]) + (sum[2][c] + sum[3][c]);
     out[col] = accumulate ? out[col] + s : s;
   }
 }
 
+// Tokens of a workgroup: one a wave where there are enough of them to fill the GPU so.
+int tokens_of(int32_t tokens) { return tokens >= 1024 ? kWaves : 1; }
 constexpr int kBackwardGroups = 1024;
 constexpr int32_t kMostTokens = 0x7fff0000;  // a token's number and one grid more stay below 2^31
-int backward_groups(int32_t tokens) { return (int)min((int64_t)kBackwardGroups, ((int64_t)tokens + kWaves - 1) / kWaves); }
+int64_t forward_groups(int32_t tokens) { return ((int64_t)tokens + tokens_of(tokens) - 1) / tokens_of(tokens); }
+int backward_groups(int32_t tokens) { return (int)std::min<int64_t>(kBackwardGroups, forward_groups(tokens)); }
 
 int lanes_of(int32_t dim) { return dim <= 32 ? 4 : dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
 
-// Calls f(lanes, neighbours) with both as compile-time constants.
+// Calls f(lanes, neighbours, tokens of a workgroup) with all as compile-time constants.
 template <class F>
-void with_form(const lora_qk_heads_t& h, F f) {
-  auto lanes = [&](auto nb) {
-    switch (lanes_of(h.head_dim)) {
-      case 4: f(std::integral_constant<int, 4>{}, nb); break;
-      case 8: f(std::integral_constant<int, 8>{}, nb); break;
-      case 16: f(std::integral_constant<int, 16>{}, nb); break;
-      default: f(std::integral_constant<int, 32>{}, nb); break;
-    }
+void with_form(const lora_qk_heads_t& h, int32_t tokens, F f) {
+  auto all = [&](auto lanes) {
+    auto rest = [&](auto nb) {
+      if (tokens_of(tokens) > 1) f(lanes, nb, std::integral_constant<int, kWaves>{});
+      else f(lanes, nb, std::integral_constant<int, 1>{});
+    };
+    if (h.neighbours) rest(std::true_type{});
+    else rest(std::false_type{});
   };
-  if (h.neighbours) lanes(std::true_type{});
-  else lanes(std::false_type{});
+  switch (lanes_of(h.head_dim)) {
+    case 4: all(std::integral_constant<int, 4>{}); break;
+    case 8: all(std::integral_constant<int, 8>{}); break;
+    case 16: all(std::integral_constant<int, 16>{}); break;
+    default: all(std::integral_constant<int, 32>{}); break;
+  }
 }
 
 int check_heads(const lora_qk_heads_t* h) {
@@ -368,18 +411,18 @@ int check_call(const lora_qk_heads_t* h, const int32_t* positions, int32_t token
 QKArgs args_of(const lora_qk_heads_t* h, const void* q, int64_t ldq, const void* k, int64_t ldk, const int32_t* positions,
                int32_t tokens, void* oq, int64_t ldoq, void* ok, int64_t ldok) {
   QKArgs a{};
-  a.q = static_cast<const uint16_t*>(q); a.ldq = ldq;
-  a.k = static_cast<const uint16_t*>(k); a.ldk = ldk;
-  a.oq = static_cast<uint16_t*>(oq); a.ldoq = ldoq;
-  a.ok = static_cast<uint16_t*>(ok); a.ldok = ldok;
-  a.wq = static_cast<const uint16_t*>(h->weight_q);
-  a.wk = static_cast<const uint16_t*>(h->weight_k);
+  a.x[0] = static_cast<const uint16_t*>(q); a.ldx[0] = ldq;
+  a.x[1] = static_cast<const uint16_t*>(k); a.ldx[1] = ldk;
+  a.o[0] = static_cast<uint16_t*>(oq); a.ldo[0] = ldoq;
+  a.o[1] = static_cast<uint16_t*>(ok); a.ldo[1] = ldok;
+  a.w[0] = static_cast<const uint16_t*>(h->weight_q);
+  a.w[1] = static_cast<const uint16_t*>(h->weight_k);
   a.freqs = h->freqs;
   a.positions = positions;
+  a.heads[0] = h->heads_q; a.heads[1] = h->heads_k;
   a.tokens = tokens;
-  a.heads_q = h->heads_q; a.heads = h->heads_q + h->heads_k;
   a.dim = h->head_dim; a.rot = h->rot_dim;
-  a.eps = h->eps;
+  a.eps = h->eps; a.mean = 1.f / (float)h->head_dim;
   return a;
 }
 
@@ -412,15 +455,10 @@ extern "C" int lora_qk_norm_rope(const void* q, int64_t ldq, const void* k, int6
     return set_error(LORA_INVALID_ARGUMENT, "an output that takes its input's place needs its row stride");
   QKArgs a = args_of(heads, q, ldq, k, ldk, positions, num_tokens, q_out, ldqo, k_out, ldko);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const int per = 64 / lanes_of(a.dim), groups = (a.heads + per - 1) / per;
-  const int u = (int64_t)num_tokens * groups >= 16384 ? 4 : 1;
-  a.per_token = (groups + u - 1) / u;
-  const int64_t n = ((int64_t)num_tokens * a.per_token + kWaves - 1) / kWaves;
-  if (n > kMaxGroups) return set_error(LORA_UNSUPPORTED, "%d tokens of %d heads are too many for one call", num_tokens, a.heads);
-  with_form(*heads, [&](auto lanes, auto nb) {
-    const dim3 grid((unsigned)n), blk(kThreads);
-    if (u == 4) hipLaunchKernelGGL((qk_forward_kernel<lanes(), nb(), 4>), grid, blk, 0, s, a);
-    else hipLaunchKernelGGL((qk_forward_kernel<lanes(), nb(), 1>), grid, blk, 0, s, a);
+  const int64_t n = forward_groups(num_tokens);
+  if (n > kMaxGroups) return set_error(LORA_UNSUPPORTED, "%d tokens are too many for one call", num_tokens);
+  with_form(*heads, num_tokens, [&](auto lanes, auto nb, auto w) {
+    hipLaunchKernelGGL((qk_forward_kernel<lanes(), nb(), w(), (w() > 1 ? 4 : 1)>), dim3((unsigned)n), dim3(kThreads), 0, s, a);
   });
   return launched("qk_norm_rope");
 }
@@ -462,20 +500,18 @@ extern "C" int lora_qk_norm_rope_backward(const void* q, int64_t ldq, const void
   const int groups = backward_groups(num_tokens);
   if (num_tokens) {
     QKArgs a = args_of(heads, q, ldq, k, ldk, positions, num_tokens, dq, lddq, dk, lddk);
-    a.gq = static_cast<const uint16_t*>(dq_out); a.ldgq = lddqo;
-    a.gk = static_cast<const uint16_t*>(dk_out); a.ldgk = lddko;
+    a.g[0] = static_cast<const uint16_t*>(dq_out); a.ldg[0] = lddqo;
+    a.g[1] = static_cast<const uint16_t*>(dk_out); a.ldg[1] = lddko;
     a.parts = static_cast<float*>(ws);
-    const int per = 64 / lanes_of(a.dim);
-    a.per_token = (a.heads + per - 1) / per;
-    with_form(*heads, [&](auto lanes, auto nb) {
+    with_form(*heads, num_tokens, [&](auto lanes, auto nb, auto w) {
       const dim3 grid((unsigned)groups), blk(kThreads);
-      if (dweight) hipLaunchKernelGGL((qk_backward_kernel<lanes(), nb(), true>), grid, blk, 0, s, a);
-      else hipLaunchKernelGGL((qk_backward_kernel<lanes(), nb(), false>), grid, blk, 0, s, a);
+      if (dweight) hipLaunchKernelGGL((qk_backward_kernel<lanes(), nb(), w(), true>), grid, blk, 0, s, a);
+      else hipLaunchKernelGGL((qk_backward_kernel<lanes(), nb(), w(), false>), grid, blk, 0, s, a);
     });
     if ((st = launched("qk_norm_rope_backward"))) return st;
   }
   if (dweight) {
-    hipLaunchKernelGGL(qk_weight_kernel, dim3((unsigned)((cols + 15) / 16)), dim3(256), 0, s, static_cast<const float*>(ws),
+    hipLaunchKernelGGL(qk_weight_kernel, dim3((unsigned)((cols + 15) / 16)), dim3(1024), 0, s, static_cast<const float*>(ws),
                        groups, cols, dweight, (flags & LORA_GRAD_ACCUMULATE) ? 1 : 0);
     return launched("qk_weight");
   }
