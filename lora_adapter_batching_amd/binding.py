@@ -706,6 +706,11 @@ def _qk_rows(name: str, t, heads: int, rows: int, h: QKHeads):
         return None, 0
     if t is None:
         raise ValueError(f"{name} is None, but there are {heads} heads of its kind")
+    shape = t.shape
+    if len(shape) == 2 and shape[0] > 1 and shape[0] >= rows and shape[1] == heads * h.head_dim:  # (the usual case)
+        stride, step = t.stride()
+        if step == 1 and t.dtype is _torch.bfloat16 and t.get_device() == h.dev:
+            return t.data_ptr(), stride
     return t.data_ptr(), _rows_arg(name, t, rows, heads * h.head_dim, h.dev)
 
 

@@ -135,14 +135,32 @@ struct Lane {
   }
 };
 
+// Rows that the launch touches once. NT 1: what it writes goes past the caches, NT 2:
+// what it reads too.
+template <int NT>
+__device__ __forceinline__ u32x4 ld_row(const uint16_t* p) {
+  if constexpr (NT >= 2) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  else return ld16(p);
+}
+template <int NT>
+__device__ __forceinline__ void st_row(uint16_t* p, u32x4 v) {
+  if constexpr (NT >= 1) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+  else st16(p, v);
+}
+
 // sum(x^2) past fp32's range: x is taken 2^-80 as large (its norm does not change).
 __device__ __forceinline__ bool past_range(float ss) { return !(ss < __builtin_inff()); }
 constexpr float kDown = 0x1p-80f;
 
 // A workgroup takes W tokens: one for each wave (W = 4), or one whose groups of heads
-// the waves take in turn. U groups are loaded before the first is used.
-template <int L, bool NB, int W, int U>
-__global__ __launch_bounds__(kThreads) void qk_forward_kernel(QKArgs a) {
+// the waves take in turn. U groups are loaded before the first is used. Bound by
+// memory in large batches; 32 + 8 heads of 128 columns, us (TB/s): 16384 tokens 63
+// (5.3), 4096 15.0 (5.6), 1000 6.5, 64 4.2, which is one launch and its chain of
+// loads. Angles made by every lane for itself and weights applied apart from the
+// rotation took 82 for 16384 tokens: the vector unit was busy most of that. Four
+// waves a SIMD (128 registers) instead of three: 4096 tokens 17.2 -> 15.0.
+template <int L, bool NB, int W, int U, int NT>
+__global__ __launch_bounds__(kThreads, 4) void qk_forward_kernel(QKArgs a) {
   constexpr int H = 64 / L, STEP = W > 1 ? 1 : kWaves;
   __shared__ Turns<W> turns;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -153,7 +171,7 @@ __global__ __launch_bounds__(kThreads) void qk_forward_kernel(QKArgs a) {
   auto load = [&](int kind, int g) {
     const int head = g * H + me.head;
     if (!there || !me.in || head >= a.heads[kind]) return zero16();
-    return ld16(a.x[kind] + (int64_t)token * a.ldx[kind] + (int64_t)head * a.dim + 8 * me.chunk);
+    return ld_row<NT>(a.x[kind] + (int64_t)token * a.ldx[kind] + (int64_t)head * a.dim + 8 * me.chunk);
   };
   u32x4 x[2][U], w[2];
 #pragma unroll
@@ -202,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void qk_forward_kernel(QKArgs a) {
         for (int e = 0; e < 8; ++e) f[e] = r * (f[e] * A[e] + p[e] * B[e]);
         const int head = (g + STEP * u) * H + me.head;
         if (me.in && head < a.heads[kind])
-          st16(a.o[kind] + (int64_t)token * a.ldo[kind] + (int64_t)head * a.dim + 8 * me.chunk, pack8(f));
+          st_row<NT>(a.o[kind] + (int64_t)token * a.ldo[kind] + (int64_t)head * a.dim + 8 * me.chunk, pack8(f));
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) x[kind][u] = next[u];
@@ -216,8 +234,13 @@ __global__ __launch_bounds__(kThreads) void qk_forward_kernel(QKArgs a) {
 // that a lane's share of dweight is summed over its tokens before it meets the
 // others' (in a fixed order: lanes, waves, then workgroups). The turns of a
 // workgroup's next tokens are made in the LDS half that the current ones leave.
-template <int L, bool NB, int W, bool DW>
-__global__ __launch_bounds__(kThreads) void qk_backward_kernel(QKArgs a) {
+// 32 + 8 heads of 128 columns, us (TB/s): 16384 tokens 98 without dweight (5.1),
+// 101 with it (5.0), 1000 tokens 9 and 14. The sums of dweight hold 16 registers:
+// three waves a SIMD and 768 workgroups, all of them resident (1024 in four waves
+// with fewer registers: 105); without them four waves and 1024 (in three: 4096
+// tokens 26 instead of 24).
+template <int L, bool NB, int W, bool DW, int NT>
+__global__ __launch_bounds__(kThreads, DW ? 3 : 4) void qk_backward_kernel(QKArgs a) {
   constexpr int H = 64 / L, STEP = W > 1 ? 1 : kWaves;
   __shared__ Turns<W> turns[2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -239,8 +262,8 @@ __global__ __launch_bounds__(kThreads) void qk_backward_kernel(QKArgs a) {
       const int head = g * H + me.head;
       x = d = zero16();
       if (!there || !me.in || head >= a.heads[kind]) return;
-      x = ld16(a.x[kind] + (int64_t)token * a.ldx[kind] + (int64_t)head * a.dim + 8 * me.chunk);
-      d = ld16(a.g[kind] + (int64_t)token * a.ldg[kind] + (int64_t)head * a.dim + 8 * me.chunk);
+      x = ld_row<NT>(a.x[kind] + (int64_t)token * a.ldx[kind] + (int64_t)head * a.dim + 8 * me.chunk);
+      d = ld_row<NT>(a.g[kind] + (int64_t)token * a.ldg[kind] + (int64_t)head * a.dim + 8 * me.chunk);
     };
     u32x4 x[2], d[2];
     load(0, g0, x[0], d[0]);
@@ -287,7 +310,7 @@ __global__ __launch_bounds__(kThreads) void qk_backward_kernel(QKArgs a) {
         for (int e = 0; e < 8; ++e) mw[e] = (mw[e] - f[e] * along) * r * down;
         const int head = g * H + me.head;
         if (me.in && head < a.heads[kind])
-          st16(a.o[kind] + (int64_t)token * a.ldo[kind] + (int64_t)head * a.dim + 8 * me.chunk, pack8(mw));
+          st_row<NT>(a.o[kind] + (int64_t)token * a.ldo[kind] + (int64_t)head * a.dim + 8 * me.chunk, pack8(mw));
         x[kind] = nx;
         d[kind] = nd;
       }
@@ -341,21 +364,32 @@ __global__ __launch_bounds__(1024) void qk_weight_kernel(const float* parts, int
 }
 
 // Tokens of a workgroup: one a wave where there are enough of them to fill the GPU so.
-int tokens_of(int32_t tokens) { return tokens >= 1024 ? kWaves : 1; }
-constexpr int kBackwardGroups = 1024;
+// 32 + 8 heads of 128, forward, us, one token and four: 1024 tokens 6.5 and 7.0, 2048 10.2
+// and 8.7.
+constexpr int32_t kOneTokenBelow = 2048;
+int tokens_of(int32_t tokens) { return tokens >= kOneTokenBelow ? kWaves : 1; }
 constexpr int32_t kMostTokens = 0x7fff0000;  // a token's number and one grid more stay below 2^31
 int64_t forward_groups(int32_t tokens) { return ((int64_t)tokens + tokens_of(tokens) - 1) / tokens_of(tokens); }
-int backward_groups(int32_t tokens) { return (int)std::min<int64_t>(kBackwardGroups, forward_groups(tokens)); }
+// Workgroups of the gradient: as many as run at once. With dweight and one token each, fewer,
+// as their shares are all read again (1000 tokens: 512 take 13.8 us, 1024 16.7, 256 16.5).
+int backward_groups(int32_t tokens, bool dw) {
+  return (int)std::min<int64_t>(!dw ? 1024 : tokens_of(tokens) > 1 ? 768 : 512, forward_groups(tokens));
+}
+// Large batches pass the caches: what they write from kOneTokenBelow tokens on (4096 tokens 17
+// -> 15 us), what they read too where all of it exceeds the Infinity Cache (16384 tokens,
+// forward 66 -> 63, gradient 111 -> 105; 4096 tokens forward 15.0 -> 16.5).
+constexpr int64_t kInfinityCache = 256 << 20;
 
 int lanes_of(int32_t dim) { return dim <= 32 ? 4 : dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
 
-// Calls f(lanes, neighbours, tokens of a workgroup) with all as compile-time constants.
+// Calls f(lanes, neighbours, tokens of a workgroup, NT) with all as compile-time constants.
 template <class F>
-void with_form(const lora_qk_heads_t& h, int32_t tokens, F f) {
+void with_form(const lora_qk_heads_t& h, int32_t tokens, int64_t bytes, F f) {
   auto all = [&](auto lanes) {
     auto rest = [&](auto nb) {
-      if (tokens_of(tokens) > 1) f(lanes, nb, std::integral_constant<int, kWaves>{});
-      else f(lanes, nb, std::integral_constant<int, 1>{});
+      if (tokens_of(tokens) == 1) f(lanes, nb, std::integral_constant<int, 1>{}, std::integral_constant<int, 0>{});
+      else if (bytes < kInfinityCache) f(lanes, nb, std::integral_constant<int, kWaves>{}, std::integral_constant<int, 1>{});
+      else f(lanes, nb, std::integral_constant<int, kWaves>{}, std::integral_constant<int, 2>{});
     };
     if (h.neighbours) rest(std::true_type{});
     else rest(std::false_type{});
@@ -366,6 +400,10 @@ void with_form(const lora_qk_heads_t& h, int32_t tokens, F f) {
     case 16: all(std::integral_constant<int, 16>{}); break;
     default: all(std::integral_constant<int, 32>{}); break;
   }
+}
+// Bytes of one matrix of all heads' rows.
+int64_t rows_bytes(const lora_qk_heads_t& h, int32_t tokens) {
+  return (int64_t)tokens * ((int64_t)h.heads_q + h.heads_k) * h.head_dim * 2;
 }
 
 int check_heads(const lora_qk_heads_t* h) {
@@ -457,8 +495,8 @@ extern "C" int lora_qk_norm_rope(const void* q, int64_t ldq, const void* k, int6
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t n = forward_groups(num_tokens);
   if (n > kMaxGroups) return set_error(LORA_UNSUPPORTED, "%d tokens are too many for one call", num_tokens);
-  with_form(*heads, num_tokens, [&](auto lanes, auto nb, auto w) {
-    hipLaunchKernelGGL((qk_forward_kernel<lanes(), nb(), w(), (w() > 1 ? 4 : 1)>), dim3((unsigned)n), dim3(kThreads), 0, s, a);
+  with_form(*heads, num_tokens, 2 * rows_bytes(*heads, num_tokens), [&](auto lanes, auto nb, auto w, auto nt) {
+    hipLaunchKernelGGL((qk_forward_kernel<lanes(), nb(), w(), (w() > 1 ? 4 : 1), nt()>), dim3((unsigned)n), dim3(kThreads), 0, s, a);
   });
   return launched("qk_norm_rope");
 }
@@ -468,7 +506,7 @@ extern "C" int lora_workspace_size_qk(const lora_qk_heads_t* heads, int32_t num_
   const int st = check_heads(heads);
   if (st) return st;
   if (!bytes || num_tokens < 0) return set_error(LORA_INVALID_ARGUMENT, "bytes is NULL or num_tokens (%d) below 0", num_tokens);
-  *bytes = (size_t)backward_groups(num_tokens) * 2 * (size_t)heads->head_dim * sizeof(float);
+  *bytes = (size_t)backward_groups(num_tokens, true) * 2 * (size_t)heads->head_dim * sizeof(float);
   return LORA_OK;
 }
 
@@ -489,7 +527,7 @@ extern "C" int lora_qk_norm_rope_backward(const void* q, int64_t ldq, const void
         (heads->heads_q && heads->heads_k && (dq == dk || dq == k || dq == dk_out || dk == q || dk == dq_out)))
       return set_error(LORA_INVALID_ARGUMENT, "a gradient starts at an input or at the other gradient");
     if (dweight) {
-      const size_t need = (size_t)backward_groups(num_tokens) * 2 * (size_t)heads->head_dim * sizeof(float);
+      const size_t need = (size_t)backward_groups(num_tokens, true) * 2 * (size_t)heads->head_dim * sizeof(float);
       if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15u)) return set_error(LORA_INVALID_ARGUMENT, "workspace is NULL or not 16-byte aligned");
       if (ws_bytes < need)
         return set_error(LORA_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, %zu are needed", ws_bytes, need);
@@ -497,20 +535,21 @@ extern "C" int lora_qk_norm_rope_backward(const void* q, int64_t ldq, const void
   }
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int cols = 2 * heads->head_dim;
-  const int groups = backward_groups(num_tokens);
+  const int groups = backward_groups(num_tokens, dweight != nullptr);
   if (num_tokens) {
     QKArgs a = args_of(heads, q, ldq, k, ldk, positions, num_tokens, dq, lddq, dk, lddk);
     a.g[0] = static_cast<const uint16_t*>(dq_out); a.ldg[0] = lddqo;
     a.g[1] = static_cast<const uint16_t*>(dk_out); a.ldg[1] = lddko;
     a.parts = static_cast<float*>(ws);
-    with_form(*heads, num_tokens, [&](auto lanes, auto nb, auto w) {
+    with_form(*heads, num_tokens, 3 * rows_bytes(*heads, num_tokens), [&](auto lanes, auto nb, auto w, auto nt) {
       const dim3 grid((unsigned)groups), blk(kThreads);
-      if (dweight) hipLaunchKernelGGL((qk_backward_kernel<lanes(), nb(), w(), true>), grid, blk, 0, s, a);
-      else hipLaunchKernelGGL((qk_backward_kernel<lanes(), nb(), w(), false>), grid, blk, 0, s, a);
+      if (dweight) hipLaunchKernelGGL((qk_backward_kernel<lanes(), nb(), w(), true, nt()>), grid, blk, 0, s, a);
+      else hipLaunchKernelGGL((qk_backward_kernel<lanes(), nb(), w(), false, nt()>), grid, blk, 0, s, a);
     });
     if ((st = launched("qk_norm_rope_backward"))) return st;
   }
   if (dweight) {
+    // (no tokens: no shares, and zeros or nothing to add)
     hipLaunchKernelGGL(qk_weight_kernel, dim3((unsigned)((cols + 15) / 16)), dim3(1024), 0, s, static_cast<const float*>(ws),
                        groups, cols, dweight, (flags & LORA_GRAD_ACCUMULATE) ? 1 : 0);
     return launched("qk_weight");
