@@ -848,5 +848,17 @@ def inspect_matmul(num_tokens: int, width: int, h_out: int) -> CMatmulKernel:
     return out
 
 
+def inspect_matmul4(x_bits: int, num_tokens: int, width: int, h_out: int) -> CMatmulKernel:
+    """Host-only: the kernel that q4_matmul launches for these sizes, on 8-bit
+    rows (x_bits = 8) or 4-bit ones."""
+    lib = load()
+    fn = lib.lora_inspect_matmul4
+    fn.restype = ctypes.c_int
+    fn.argtypes = [ctypes.c_int32] * 4 + [ctypes.POINTER(CMatmulKernel)]
+    out = CMatmulKernel()
+    _check(fn(int(x_bits), int(num_tokens), int(width), int(h_out), ctypes.byref(out)))
+    return out
+
+
 def version() -> int:
     return int(load().lora_version())

@@ -95,6 +95,9 @@ typedef struct lora_matmul_kernel_t {
   int32_t exps;            /* blocks whose exponents LDS holds at a time (0: none are staged) */
 } lora_matmul_kernel_t;
 int lora_inspect_matmul(int32_t num_tokens, int32_t width, int32_t h_out, lora_matmul_kernel_t* out);
+/* The same of the product on 4-bit weights: of lora_q4_matmul_q8() with
+ * x_bits = 8, of lora_q4_matmul() with 4. */
+int lora_inspect_matmul4(int32_t x_bits, int32_t num_tokens, int32_t width, int32_t h_out, lora_matmul_kernel_t* out);
 
 #ifdef __cplusplus
 }

@@ -691,3 +691,23 @@ extern "C" int lora_q4_matmul_q8(const lora_q8_t* x, const lora_q4_t* w, void* y
   a.x = x->values; a.ldx = x->ld; a.xe = x->exps; a.ldxe = x->ld_exps;
   return product(a, true, w, x->rows, x->width, x->values, y, ldy, flags, stream);
 }
+
+// Host-only: the kernel that a product takes (lora_inspect.h)
+extern "C" int lora_inspect_matmul4(int32_t x_bits, int32_t num_tokens, int32_t width, int32_t h_out, lora_matmul_kernel_t* out) {
+  clear_error();
+  if (!out || (x_bits != 8 && x_bits != 4)) return set_error(LORA_INVALID_ARGUMENT, "out is NULL or x_bits (%d) not 8 or 4", x_bits);
+  if (num_tokens <= 0 || width <= 0 || h_out <= 0 || (width & 7) || (h_out & 7))
+    return set_error(LORA_INVALID_ARGUMENT, "num_tokens (%d), width (%d) and h_out (%d) must be positive, the widths multiples of 8",
+                     num_tokens, width, h_out);
+  const int32_t nkb = (int32_t)q4_panels(width);
+  const TileChoice* c = choose(x_bits == 8, num_tokens, h_out, nkb);
+  out->kernels = 1 + kTileCount;
+  out->kernel = c ? 1 + (int32_t)(c - (x_bits == 8 ? kTiles8 : kTiles4)) : 0;
+  out->tokens = c ? c->bt : kFewTokens;
+  out->columns = c ? c->bn : 16;
+  out->groups = c ? c->ks : kFewWaves;
+  out->stages = c ? c->stages : 0;
+  out->blocks = (nkb + out->groups - 1) / out->groups;
+  out->exps = c && x_bits == 8 ? kExpBlocks : 0;
+  return LORA_OK;
+}
