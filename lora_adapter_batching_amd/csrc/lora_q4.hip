@@ -16,8 +16,9 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// A workgroup takes 4 panels of 4 U rows: each wave reads 1 KB runs of one row
-// and writes the panels' rows 4 w .. 4 w + 3, which follow each other.
+// A workgroup takes 4 panels of 4 kRows rows: each wave reads 1 KB runs of one row
+// and writes neighbouring rows of the panels, which follow each other.
+constexpr int kRows = 2;  // of a wave, loaded together (one, four, eight: 5, 2, 9% slower to store 32768 x 4096)
 struct Q4Args {
   const uint16_t* x;  // quantise: source; restore: target (cast)
   int64_t ldx;
@@ -33,15 +34,18 @@ struct Q4Args {
 struct Place {
   int row0, panel, chunk;
 };
-template <int U>
 __device__ __forceinline__ Place place_of(const Q4Args& a) {
   const int tr = blockIdx.x / a.tiles_p, tp = blockIdx.x - tr * a.tiles_p;
-  return Place{(tr * 4 + (int)(threadIdx.x >> 6)) * U, tp * 4 + ((int)(threadIdx.x >> 4) & 3), (int)threadIdx.x & 15};
+  return Place{(tr * 4 + (int)(threadIdx.x >> 6)) * kRows, tp * 4 + ((int)(threadIdx.x >> 4) & 3), (int)threadIdx.x & 15};
 }
 
-template <int U>
+// us (TB/s), x past the caches (NT) where it is too large for them: 256 x 2560 2.3, 2560 x
+// 2560 4.4, 8192 x 4096 14.1 (6.0; 16.3 with NT: x was in the Infinity Cache), 19456
+// x 2560 23.6 (5.4; 24.8 without), 32768 x 4096 55 (6.1; 58).
+template <bool NT>
 __global__ __launch_bounds__(kThreads) void q4_rows_kernel(Q4Args a) {
-  const Place p = place_of<U>(a);
+  constexpr int U = kRows;
+  const Place p = place_of(a);
   const int col = p.panel * kQ4Panel + 8 * p.chunk;
   u32x4 v[U];
 #pragma unroll
@@ -49,7 +53,7 @@ __global__ __launch_bounds__(kThreads) void q4_rows_kernel(Q4Args a) {
     v[u] = zero16();
     if (p.row0 + u < a.rows && col < a.width) {
       const uint16_t* src = a.x + (int64_t)(p.row0 + u) * a.ldx + col;
-      if constexpr (U > 1) v[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src));
+      if constexpr (NT) v[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src));
       else v[u] = ld16(src);
     }
   }
@@ -68,9 +72,13 @@ __global__ __launch_bounds__(kThreads) void q4_rows_kernel(Q4Args a) {
   }
 }
 
-template <int U>
+// us (TB/s), the restored rows past the caches (NT) in all but small matrices: 256 x 2560
+// 2.5, 2048 x 4096 3.8 (5.7; 5.0 without NT), 19456 x 2560 19.7 (6.4; 26), 32768 x 4096
+// 48 (7.0; 62).
+template <bool NT>
 __global__ __launch_bounds__(kThreads) void q4_restore_kernel(Q4Args a) {
-  const Place p = place_of<U>(a);
+  constexpr int U = kRows;
+  const Place p = place_of(a);
   const int col = p.panel * kQ4Panel + 8 * p.chunk;
   if (col >= a.width) return;
   uint32_t q[U], e[U];
@@ -88,14 +96,14 @@ __global__ __launch_bounds__(kThreads) void q4_restore_kernel(Q4Args a) {
     if (p.row0 + u >= a.rows) return;
     u32x4* dst = reinterpret_cast<u32x4*>(const_cast<uint16_t*>(a.x) + (int64_t)(p.row0 + u) * a.ldx + col);
     const u32x4 r = restore_e2m1(q[u], e[u]);
-    if constexpr (U > 1) __builtin_nontemporal_store(r, dst);
+    if constexpr (NT) __builtin_nontemporal_store(r, dst);
     else *dst = r;
   }
 }
 
 // Weights in both orientations: one workgroup per 128 x 128 block (a panel of
 // each store), the scale shared by 32 x 32 values so that both hold the same
-// numbers.
+// numbers. us (TB/s): 2560 x 2560 7.4, 19456 x 2560 32.5 (4.7), 32768 x 4096 79 (5.2).
 struct Q4PairArgs {
   Q4Args a;
   uint8_t* values_t;
@@ -178,9 +186,10 @@ __global__ __launch_bounds__(kThreads) void q4_pair_kernel(Q4PairArgs b) {
   }
 }
 
-// Large matrices (8 M values) keep 4 rows per thread in flight and stream.
-constexpr int kManyRows = 4;
-bool many(int64_t rows, int64_t width) { return rows * width >= (int64_t)8 << 20; }
+// Matrices whose bf16 rows pass the caches: read from 80 MB on, written from 8 MB on (the
+// times are at the kernels).
+constexpr int64_t kStreamRead = (int64_t)40 << 20, kStreamWrite = (int64_t)4 << 20;  // values
+bool at_least(const lora_q4_t* q, int64_t values) { return (int64_t)q->rows * q->width >= values; }
 
 // A launch holds fewer than 2^32 threads.
 constexpr int64_t kMaxGroups = 0xffffffffll / kThreads;
@@ -200,10 +209,7 @@ Q4Args args_of(const void* x, int64_t ldx, const lora_q4_t* q) {
   a.tiles_p = (a.panels + 3) / 4;
   return a;
 }
-int64_t tiles(const Q4Args& a, bool m) {
-  const int64_t per = m ? 4 * kManyRows : 4;
-  return ((int64_t)a.rows + per - 1) / per * a.tiles_p;
-}
+int64_t tiles(const Q4Args& a) { return ((int64_t)a.rows + 4 * kRows - 1) / (4 * kRows) * a.tiles_p; }
 
 }  // namespace
 
@@ -256,11 +262,10 @@ extern "C" int lora_q4_quantize(const void* x, int64_t ldx, const lora_q4_t* out
     hipLaunchKernelGGL(q4_pair_kernel, dim3((unsigned)n), dim3(kThreads), 0, s, b);
     return launched("q4_pair");
   }
-  const bool m = many(out->rows, out->width);
-  const int64_t n = tiles(a, m);
+  const int64_t n = tiles(a);
   if (n > kMaxGroups) return set_error(LORA_UNSUPPORTED, "x of %d x %d is too large for one call", out->rows, out->width);
-  if (m) hipLaunchKernelGGL(q4_rows_kernel<kManyRows>, dim3((unsigned)n), dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL(q4_rows_kernel<1>, dim3((unsigned)n), dim3(kThreads), 0, s, a);
+  if (at_least(out, kStreamRead)) hipLaunchKernelGGL(q4_rows_kernel<true>, dim3((unsigned)n), dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL(q4_rows_kernel<false>, dim3((unsigned)n), dim3(kThreads), 0, s, a);
   return launched("q4_rows");
 }
 
@@ -272,11 +277,10 @@ extern "C" int lora_q4_dequantize(const lora_q4_t* q, void* x, int64_t ldx, void
   if ((st = check_bf16_rows(x, ldx, q->width, "x"))) return st;
   if (x == q->values) return set_error(LORA_INVALID_ARGUMENT, "x starts at the store");
   const Q4Args a = args_of(x, ldx, q);
-  const bool m = many(q->rows, q->width);
-  const int64_t n = tiles(a, m);
+  const int64_t n = tiles(a);
   if (n > kMaxGroups) return set_error(LORA_UNSUPPORTED, "q of %d x %d is too large for one call", q->rows, q->width);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (m) hipLaunchKernelGGL(q4_restore_kernel<kManyRows>, dim3((unsigned)n), dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL(q4_restore_kernel<1>, dim3((unsigned)n), dim3(kThreads), 0, s, a);
+  if (at_least(q, kStreamWrite)) hipLaunchKernelGGL(q4_restore_kernel<true>, dim3((unsigned)n), dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL(q4_restore_kernel<false>, dim3((unsigned)n), dim3(kThreads), 0, s, a);
   return launched("q4_restore");
 }

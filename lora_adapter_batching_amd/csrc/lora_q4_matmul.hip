@@ -114,6 +114,24 @@ __device__ __forceinline__ void tile_of(const Mat4Args& a, int b, int grid, int&
 // rows on distinct banks. The loads write LDS directly, so the permutation is
 // applied to the address that each lane reads from.
 //
+// What bounds the 256 x 256 tile: a panel is 1024 clocks of the matrix unit in 4 bits
+// (2048 with 8-bit x); its 34 (50) KB take the load path half of that, and the
+// fragments' reads and the loads' writes 784 (1100) of LDS. So
+//  - a half panel's fragments are read in its first half's instructions, so that
+//    none is waited for where the waves meet, and the next stage's loads are spread
+//    over the rest of both halves: 0.915 -> 0.835 us a panel in 4 bits,
+//  - addresses are walked by scalar additions,
+//  - three stages: 250 -> 232 us for 8192 tokens 4096 -> 14336 in 4 bits (four: 238), 98
+//    -> 90 for 8191 tokens 4096 -> 4096 with 8-bit x (two stages),
+//  - y leaves by non-temporal stores: all CUs end their tiles at about the same time.
+// 8192 tokens 4096 -> 14336: 232-236 us in 4 bits (4.1 PFLOP/s), 316-327 with 8-bit x
+// (3.0); the library's product of 4-bit operands reaches 3.0 for 8192^3. In the steps
+// it is 4.7 PFLOP/s on random values and 7.2 on constant ones, which is the rate of
+// the matrix instructions alone (7.1): the clock under load is the bound. Each tile's
+// start and end are 6.4 us of 33; workgroups that walk over the tiles and load the
+// next one's first stages under them took as long in 4 bits (234 us) and longer with
+// 8-bit x (99 us instead of 93 for 8191 tokens 4096 -> 4096).
+//
 // Exponents of 8-bit rows (one for each 128 columns, row after row in memory) are
 // fetched once for kExpBlocks blocks, as a row's dwords are far apart.
 //
@@ -478,7 +496,10 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
 // Few tokens: the weights are read once and that is the floor. A workgroup
 // owns 16 columns and up to 16 tokens; its 8 waves take every eighth panel of
 // the sum straight from memory into fragments (16 rows of a panel are one run of
-// 1 KB) and their parts are added in wave order.
+// 1 KB) and their parts are added in wave order. 1 token (8-bit x), us: 2560 -> 2560 2.8,
+// which is one launch, 2560 -> 19456 6.4 (4.1 TB/s), 9728 -> 2560 5.8 (ten panels a
+// wave, one behind the other). Two to four panels in flight a wave or 16 waves were
+// slower (6.4 -> 7.1-9.4 for 2560 -> 19456).
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
 constexpr int kFewTokens = 16;
@@ -554,22 +575,21 @@ void launch_few(const Mat4Args& a, bool add, hipStream_t s) {
 
 // Tiles to choose from. A workgroup of a tile takes about fixed + step * (its
 // panels of the sum) microseconds while `slots` of them run, so a product takes
-// that times the rounds its tiles need: a fit to these times on 256 CUs (us; tiles
-// by tokens x columns, / the groups that share the sum; 8-bit x, then 4-bit x).
-//   tokens, k, n        256x256    256x128    128x160    128x128     128x96      64x64    64x96/2    64x64/4    32x64/4    32x32/4
-//   37, 2560, 2560                                                           7.1   5.8  7.1   6.4  6.6   5.5  5.0   4.5  4.4   3.9
-//   37, 9728, 2560                                                          20.1  15.2 16.1  14.6 13.0  10.2  9.9   8.7  8.0   6.5
-//   100, 9728, 2560                                                         20.1  15.3 16.7  14.7 13.6  10.3 10.2   8.8 14.0   9.2
-//   128, 2560, 19456                         12.5  11.1 11.4  9.8 10.4  9.4 15.1  10.4 14.7  10.6
-//   256, 9728, 2560                                                         20.2  15.4 17.0  14.9 14.2  10.9 19.4  13.6 20.9  14.3
-//   256, 2560, 19456              17.5 13.2  14.7  12.7 18.0 13.5 18.0 13.5 21   16    24    17
-//   512, 2560, 2560                                     10.7  9.0 10.0  9.0  9.0   7.7  7.9   7.0 11.9   7.9
-//   512, 4096, 14336              27.0 21.5  34.5  29   28   22   39   28
-//   2048, 4096, 4096              28.5 22.1  34.9  25.5 29.1 24.1 35.4 25.5
-//   8191, 4096, 4096   94   69   117   75   138    94   115   80
-//   8192, 4096, 14336  324  236  398  249   454   320   386  276
-// Over the 34 products measured for it the choice is the fastest tile of the list or within
-// 7% of it. Nothing in the fit stands for the weights' bytes.
+// that times the rounds its tiles need: a fit to these times on 256 CUs (us, 8-bit x /
+// 4-bit x; tiles are tokens x columns, :n the groups of waves that share the sum).
+//   37, 2560, 2560       64x64 7.1/5.8    64x96:2 7.1/6.5   64x64:4 6.6/5.5    32x64:4 5.0/4.5    32x32:4 4.4/3.9
+//   37, 9728, 2560       64x64 20.1/15.2  64x96:2 16.1/14.6 64x64:4 13.0/10.2  32x64:4 9.9/8.7    32x32:4 8.0/6.5
+//   100, 9728, 2560      64x64 20.1/15.3  64x96:2 16.7/14.7 64x64:4 13.6/10.3  32x64:4 10.2/8.8   32x32:4 14.0/9.2
+//   128, 2560, 19456     128x160 12.6/11.0 128x128 11.4/9.8 128x96 10.5/9.4    64x64 15.1/10.6    64x96:2 14.7/10.6
+//   256, 9728, 2560      64x64 20.2/15.4  64x96:2 17.0/14.9 64x64:4 14.2/10.9  32x64:4 19.4/13.6  32x32:4 20.9/14.3
+//   256, 2560, 19456     256x128 17.5/13.2 128x160 14.7/12.7 128x128 18.0/13.5 128x96 19.3/13.5   64x64 22.3/16.0
+//   512, 2560, 2560      128x128 10.7/9.2 128x96 10.0/9.0   64x64 9.0/7.7      64x96:2 7.9/7.0    64x64:4 13.0/10.5
+//   512, 4096, 14336     256x128 27.0/21.5 128x160 34.5/29.0 128x128 28.1/22.0 128x96 40.5/28.4
+//   2048, 4096, 4096     256x128 28.5/22.1 128x160 34.9/29.8 128x128 29.1/24.1 128x96 41.5/29.4
+//   8191, 4096, 4096     256x256 94/69    256x128 117/75    128x160 138/113    128x128 115/80
+//   8192, 4096, 14336    256x256 324/236  256x128 398/249   128x160 454/379    128x128 386/276
+// Over the 34 products it is made from, the choice is the fastest tile of the list or within
+// 7% of it. Nothing in it stands for the weights' bytes.
 struct TileChoice {
   int bt, bn, ks, stages, slots;
   float fixed, step;
