@@ -8,7 +8,7 @@ PRODUCTS = [
     (4, 7, 1352, 1000), (4, 16, 9736, 264), (8, 7, 1352, 1000), (8, 13, 9736, 264),
     (4, 650, 440, 11448), (8, 650, 440, 11448), (8, 1795, 3744, 5456),      # 256 x 256
     (4, 258, 440, 14664), (8, 258, 440, 14664), (8, 297, 3640, 14072),      # 256 x 128
-    (4, 257, 424, 11344), (8, 257, 424, 11344), (8, 257, 3960, 11704),      # 128 x 160
+    (4, 257, 616, 11344), (8, 257, 616, 11344), (8, 257, 3960, 11704),      # 128 x 160
     (4, 138, 392, 11240), (8, 138, 392, 11240), (8, 130, 3616, 14824),      # 128 x 128
     (4, 141, 912, 12216), (8, 144, 1304, 11440), (8, 137, 3864, 11896),     # 128 x 96
     (4, 65, 520, 6760), (8, 4370, 528, 72), (8, 66, 3912, 13384),           # 64 x 64
