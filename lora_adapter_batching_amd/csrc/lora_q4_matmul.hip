@@ -589,8 +589,8 @@ void launch_few(const Mat4Args& a, bool add, hipStream_t s) {
 //   8191, 4096, 4096     256x256 94/69    256x128 117/75    128x128 115/80
 //   8192, 4096, 14336    256x256 324/236  256x128 398/249   128x128 386/276
 // Over the 34 products it is made from, the choice is the fastest tile of the list or within
-// 7% of it. Nothing in it stands for the weights' bytes. (128x160 has four stages: 256, 2560,
-// 19456 takes 14.8/13.1 with three, 13.7/12.0 with five; 128x128 gains nothing from a fourth.)
+// 7% of it. Nothing in it stands for the weights' bytes. (128x160 has four stages: with its
+// operands from memory 256, 2560, 19456 takes 17.3/14.1, with three 18.0/15.4, with five 17.7/14.5.)
 struct TileChoice {
   int bt, bn, ks, stages, slots;
   float fixed, step;
