@@ -147,6 +147,15 @@ def test_binding_refuses_wrong_tensors():
                      (L.q4_matmul, (x, L.new_q8_weights(16, 256, "cpu"), bf(4, 16))), (L.q4_matmul, (L.new_q8_weights(4, 256, "cpu"), w, bf(4, 16)))]:
         with pytest.raises(ValueError):
             fn(*args)
+    # a store of the other form is no store of this one
+    for fn, args in [(L.q4_quantize, (bf(4, 256), x8)), (L.q4_quantize, (bf(4, 256), x, L.new_q8_weights(256, 4, "cpu"))),
+                     (L.q4_dequantize, (x8, bf(4, 256)))]:
+        with pytest.raises(ValueError, match="must be a Q4"):
+            fn(*args)
+    for fn, args in [(L.q8_quantize, (bf(4, 256), x)), (L.q8_dequantize, (x, bf(4, 256))), (L.q8_matmul, (x8, w, bf(4, 16))),
+                     (L.swiglu, (bf(4, 512), None, x))]:
+        with pytest.raises(AttributeError):
+            fn(*args)
     for fn, args in [(L.q4_quantize, (bf(4, 256), x)), (L.q4_matmul, (x, w, bf(4, 16))), (L.q4_matmul, (x8, w, bf(4, 16)))]:
         with pytest.raises(ValueError, match="device tensors"):
             fn(*args)
