@@ -79,7 +79,8 @@ EXPORTS = ["lora_segments_from_ids", "lora_workspace_size", "lora_sgmv_shrink", 
 NOALLOC_SCRATCH_BYTES = 16 << 20  # LORA_NOALLOC_SCRATCH_BYTES
 
 _lib = None
-_torch = None  # set by load(): the hot calls look it up once per call, not per import statement
+_torch = None  # set by load(), as are the next three: the hot calls look them up once per call, not per import statement
+_bf16 = _device_now = _stream_now = None
 
 
 def load(path: str = LIB_PATH):
@@ -93,8 +94,10 @@ def load(path: str = LIB_PATH):
     # runtime; loading it first makes the library bind to that same runtime,
     # so that one HIP runtime serves the process
     import torch
-    global _torch
-    _torch = torch
+    global _torch, _bf16, _device_now, _stream_now
+    _torch, _bf16 = torch, torch.bfloat16
+    _device_now = getattr(torch._C, "_cuda_getDevice", None)  # (missing in a torch without GPU support)
+    _stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     lib = ctypes.CDLL(path)
     P = ctypes.c_void_p
     I64 = ctypes.c_int64
@@ -478,7 +481,7 @@ def new_q8_weights(rows: int, width: int, device="cuda") -> Q8Weights:
 
 def _rows_arg(name: str, t, rows: int, width: int, dev: int) -> int:
     """The row stride of a bfloat16 [>= rows, width] tensor on GPU `dev`."""
-    if t.dtype is _torch.bfloat16 and t.get_device() == dev:
+    if t.dtype is _bf16 and t.get_device() == dev:
         shape = t.shape
         if len(shape) == 2 and shape[0] >= rows and shape[1] == width:
             stride, step = t.stride()
@@ -516,11 +519,10 @@ def _call_on(dev: int, stream, fn, *args):
         raise ValueError("device tensors are needed, got cpu")
     if stream is not None and getattr(stream, "device_index", dev) != dev:
         raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors are on cuda:{dev}")
-    cuda = _torch._C
-    if dev != cuda._cuda_getDevice():
+    if dev != _device_now():
         with _torch.cuda.device(dev):
             return _call_on(dev, stream, fn, *args)
-    st = fn(*args, cuda._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream))
+    st = fn(*args, _stream_now(dev) if stream is None else _stream_handle(stream))
     if st:
         _check(st)
 
@@ -693,6 +695,7 @@ class QKHeads:
                  neighbours: bool = False):
         import torch
         self.heads_q, self.heads_k, self.head_dim = int(heads_q), int(heads_k), int(head_dim)
+        self.width_q, self.width_k = self.heads_q * self.head_dim, self.heads_k * self.head_dim
         for name, t, n, dtype in (("weight_q", weight_q, self.head_dim if self.heads_q else 0, torch.bfloat16),
                                   ("weight_k", weight_k, self.head_dim if self.heads_k else 0, torch.bfloat16),
                                   ("freqs", freqs, None, torch.float64)):
@@ -712,18 +715,19 @@ class QKHeads:
         self.addr = ctypes.addressof(self._c)
 
 
-def _qk_rows(name: str, t, heads: int, rows: int, h: QKHeads):
+def _qk_rows(name: str, t, width: int, rows: int, dev: int):
     """(address, row stride) of the rows of one kind of heads."""
-    if not heads:
+    if not width:
         return None, 0
     if t is None:
-        raise ValueError(f"{name} is None, but there are {heads} heads of its kind")
-    shape = t.shape
-    if len(shape) == 2 and shape[0] > 1 and shape[0] >= rows and shape[1] == heads * h.head_dim:  # (the usual case)
-        stride, step = t.stride()
-        if step == 1 and t.dtype is _torch.bfloat16 and t.get_device() == h.dev:
-            return t.data_ptr(), stride
-    return t.data_ptr(), _rows_arg(name, t, rows, heads * h.head_dim, h.dev)
+        raise ValueError(f"{name} is None, but there are heads of its kind")
+    if t.dtype is _bf16 and t.get_device() == dev:
+        shape = t.shape
+        if len(shape) == 2 and shape[0] >= rows and shape[0] > 1 and shape[1] == width:  # (the usual case)
+            stride, step = t.stride()
+            if step == 1:
+                return t.data_ptr(), stride
+    return t.data_ptr(), _rows_arg(name, t, rows, width, dev)
 
 
 def _qk_positions(positions, dev: int) -> int:
@@ -738,9 +742,9 @@ def qk_norm_rope(q, k, heads: QKHeads, positions, q_out, k_out, stream=None):
     rotation by positions [T], into q_out and k_out (which may be q and k)."""
     lib, h = _lib or load(), heads
     T = _qk_positions(positions, h.dev)
-    _call_on(h.dev, stream, lib.lora_qk_norm_rope, *_qk_rows("q", q, h.heads_q, T, h), *_qk_rows("k", k, h.heads_k, T, h),
-             h.addr, positions.data_ptr(), T, *_qk_rows("q_out", q_out, h.heads_q, T, h),
-             *_qk_rows("k_out", k_out, h.heads_k, T, h))
+    _call_on(h.dev, stream, lib.lora_qk_norm_rope, *_qk_rows("q", q, h.width_q, T, h.dev), *_qk_rows("k", k, h.width_k, T, h.dev),
+             h.addr, positions.data_ptr(), T, *_qk_rows("q_out", q_out, h.width_q, T, h.dev),
+             *_qk_rows("k_out", k_out, h.width_k, T, h.dev))
 
 
 def new_workspace_qk(heads: QKHeads, num_tokens: int):
@@ -764,10 +768,10 @@ def qk_norm_rope_backward(q, k, heads: QKHeads, positions, dq_out, dk_out, dq, d
     if ws is not None and ws.get_device() != h.dev:
         raise ValueError(f"ws is on {ws.device}, expected {_dev_name(h.dev)}")
     wp, wb = _ws(ws)
-    _call_on(h.dev, stream, lib.lora_qk_norm_rope_backward, *_qk_rows("q", q, h.heads_q, T, h),
-             *_qk_rows("k", k, h.heads_k, T, h), h.addr, positions.data_ptr(), T,
-             *_qk_rows("dq_out", dq_out, h.heads_q, T, h), *_qk_rows("dk_out", dk_out, h.heads_k, T, h),
-             *_qk_rows("dq", dq, h.heads_q, T, h), *_qk_rows("dk", dk, h.heads_k, T, h),
+    _call_on(h.dev, stream, lib.lora_qk_norm_rope_backward, *_qk_rows("q", q, h.width_q, T, h.dev),
+             *_qk_rows("k", k, h.width_k, T, h.dev), h.addr, positions.data_ptr(), T,
+             *_qk_rows("dq_out", dq_out, h.width_q, T, h.dev), *_qk_rows("dk_out", dk_out, h.width_k, T, h.dev),
+             *_qk_rows("dq", dq, h.width_q, T, h.dev), *_qk_rows("dk", dk, h.width_k, T, h.dev),
              _ptr(dweight), int(flags), wp, wb)
 
 
