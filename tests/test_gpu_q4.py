@@ -84,6 +84,34 @@ def test_quantize_bit_exact(T, W):
     assert torch.all(big[T] == 5) and torch.all(big[:, W:] == 5)
 
 
+@pytest.mark.parametrize("T,W", [(20003, 2104), (5001, 8264)])
+def test_large_matrices_are_stored_as_their_parts(T, W):
+    """Matrices past the caches take kernels of their own: the same bytes as
+    the rows in parts, and nothing behind them."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    x = torch.randn((T, W), generator=g, device="cuda").mul_(torch.exp(torch.randn((T, 1), generator=g, device="cuda"))).to(torch.bfloat16)
+    x[T // 2, 40], x[T - 1, W - 1] = float("nan"), float("inf")
+    q, parts = wide_q4(T, W), L.new_q4(T, W)
+    L.q4_quantize(x, q)
+    big, out = strided(torch.zeros_like(x), fill=5.0)
+    L.q4_dequantize(q, out)
+    back = torch.zeros_like(x)
+    for a in range(0, T, 400):
+        b = min(T, a + 400)
+        part = L.Q4(parts.values[:, a:b], parts.exps[:, a:b], W)
+        L.q4_quantize(x[a:b], part)
+        L.q4_dequantize(part, back[a:b])
+    n = R.panels(W)                                                  # (the last panel of the larger store is not ours)
+    assert bool((q.values[:n] == parts.values).all()) and bool((q.exps[:n] == parts.exps).all())
+    assert torch.equal(out.nan_to_num(7.0), back.nan_to_num(7.0)) and torch.equal(out.isnan(), back.isnan())
+    assert torch.all(big[T] == 5) and torch.all(big[:, W:] == 5)
+    v, e = q.whole
+    v[:n, 4:4 + T], e[:n, 4:4 + T] = 0xAB, 255
+    assert torch.all(v == 0xAB) and torch.all(e == 255)
+    check_store(L.Q4(parts.values[:, :90], parts.exps[:, :90], W), to_f64(x[:90]))
+
+
 def test_quantize_every_bf16_value():
     """Each bf16 pattern as the largest of its block, beside fixed fractions of it (ties among them)."""
     bits = np.arange(65536, dtype=np.uint32).astype(np.uint16)
