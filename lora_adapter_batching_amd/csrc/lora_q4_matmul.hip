@@ -126,11 +126,14 @@ __device__ __forceinline__ void tile_of(const Mat4Args& a, int b, int grid, int&
 //  - y leaves by non-temporal stores: all CUs end their tiles at about the same time.
 // 8192 tokens 4096 -> 14336: 232-236 us in 4 bits (4.1 PFLOP/s), 316-327 with 8-bit x
 // (3.0); the library's product of 4-bit operands reaches 3.0 for 8192^3. In the steps
-// it is 4.7 PFLOP/s on random values and 7.2 on constant ones, which is the rate of
-// the matrix instructions alone (7.1): the clock under load is the bound. Each tile's
-// start and end are 6.4 us of 33; workgroups that walk over the tiles and load the
-// next one's first stages under them took as long in 4 bits (234 us) and longer with
-// 8-bit x (99 us instead of 93 for 8191 tokens 4096 -> 4096).
+// it is 4.7 PFLOP/s on random values and 7.2 on constant ones. The launch takes 436
+// thousand clocks on either, the matrix unit busy in 53% of them, at 1.9 GHz on random
+// and 2.4 on constant values: power sets the clock, and fewer clocks are in part paid
+// back by a lower one. (The matrix instructions alone, from registers, reach 6.8-7.0
+// PFLOP/s on random values at 1.7 GHz and 9.0 on constant ones at 2.3; with 8-bit x
+// 4.0-4.2 and 4.9.) Each tile's start and end are 6.4 us of 33; workgroups that walk
+// over the tiles and load the next one's first stages under them took as long in 4 bits
+// (234 us) and longer with 8-bit x (99 us instead of 93 for 8191 tokens 4096 -> 4096).
 //
 // Exponents of 8-bit rows (one for each 128 columns, row after row in memory) are
 // fetched once for kExpBlocks blocks, as a row's dwords are far apart.
