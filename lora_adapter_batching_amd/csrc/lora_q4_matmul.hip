@@ -123,7 +123,10 @@ __device__ __forceinline__ void tile_of(const Mat4Args& a, int b, int grid, int&
 //  - addresses are walked by scalar additions,
 //  - three stages: 250 -> 232 us for 8192 tokens 4096 -> 14336 in 4 bits (four: 238), 98
 //    -> 90 for 8191 tokens 4096 -> 4096 with 8-bit x (two stages),
-//  - y leaves by non-temporal stores: all CUs end their tiles at about the same time.
+//  - y leaves by non-temporal stores: all CUs end their tiles at about the same time; and
+//    what is added to comes by non-temporal loads: 284 -> 271 us (y +=, 4 bits), 112 -> 106
+//    (8191 tokens, 8-bit x). (Its lines touched 3 to 12 panels before the end, to have them
+//    in L2 by then, was 2-5% slower.)
 // 8192 tokens 4096 -> 14336: 232-236 us in 4 bits (4.1 PFLOP/s), 316-327 with 8-bit x
 // (3.0); the library's product of 4-bit operands reaches 3.0 for 8192^3. In the steps
 // it is 4.7 PFLOP/s on random values and 7.2 on constant ones. The launch takes 436
@@ -461,7 +464,8 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
         int r, c;
         uint16_t* yp;
         old[i][p] = zero16();
-        if (place(i, p, r, c, yp)) old[i][p] = ld16(yp);
+        if (place(i, p, r, c, yp))
+          old[i][p] = C::STREAM ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(yp)) : ld16(yp);
       }
   }
 #pragma unroll
