@@ -519,7 +519,7 @@ typedef struct lora_qk_heads_t {
   int32_t head_dim;     /* a multiple of 8, up to 256 */
   int32_t rot_dim;      /* a multiple of 16 from 0 (no rotation) to head_dim */
   int32_t neighbours;   /* 0: pairs (i, i + rot_dim / 2); otherwise (2 i, 2 i + 1) */
-  float eps;            /* > 0 */
+  float eps;            /* > 0 (a normal number), at most 1e30 */
   const void* weight_q; /* DEVICE bf16 [head_dim], 16-byte aligned */
   const void* weight_k;
   const double* freqs;  /* DEVICE fp64 [rot_dim / 2], radians per position */

@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kThreads, 4) void qk_forward_kernel(QKArgs a) {
   auto heads_of = [&](auto kind_) {
     constexpr int kind = decltype(kind_)::value;
     // The weight goes into the rotation: column e of the output is
-    // r (A[e] x[e] + B[e] x[its pair's other]).
+    // A[e] r x[e] + B[e] r x[its pair's other].
     float A[8], B[8];
     unpack8(w[kind], A);
     me.pairs(w[kind], A, B);
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(kThreads, 4) void qk_forward_kernel(QKArgs a) {
         }
         const float r = __builtin_amdgcn_rsqf(ss * a.mean + a.eps * down * down);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = r * (f[e] * A[e] + p[e] * B[e]);
+        for (int e = 0; e < 8; ++e) f[e] = r * f[e] * A[e] + r * p[e] * B[e];  // (x w alone can leave the range)
         const int head = (g + STEP * u) * H + me.head;
         if (me.in && head < a.heads[kind])
           st_row<NT>(a.o[kind] + (int64_t)token * a.ldo[kind] + (int64_t)head * a.dim + 8 * me.chunk, pack8(f));
@@ -228,6 +228,28 @@ __global__ __launch_bounds__(kThreads, 4) void qk_forward_kernel(QKArgs a) {
   };
   heads_of(std::integral_constant<int, 0>{});
   heads_of(std::integral_constant<int, 1>{});
+}
+
+// Weights whose largest is 2^32 and more, or below 2^-32, are taken in a unit of their own,
+// a power of two, so that their products with gradients stay in range: brings w
+// to it and returns it (1 for all others, and where one is no number).
+__device__ __forceinline__ float weight_unit(u32x4& w) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) m = max(max(m, (w[q] << 16) & 0x7fffffffu), w[q] & 0x7fff0000u);
+  constexpr uint32_t low = (127u - 32) << 23, high = (127u + 32) << 23;
+  if (__any(m >= low) && !__any(m >= high)) return 1.f;
+#pragma unroll
+  for (int l = 1; l < 64; l *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, l));
+  const uint32_t e = __builtin_amdgcn_readfirstlane(m) >> 23;
+  if (e == 0 || e == 255) return 1.f;
+  const uint32_t u = min(e, 253u);
+  float f[8];
+  unpack8(w, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] *= __builtin_bit_cast(float, (254u - u) << 23);
+  w = pack8(f);
+  return __builtin_bit_cast(float, u << 23);
 }
 
 // The gradient. The grid is bounded and its workgroups take the tokens in turn, so
@@ -247,10 +269,11 @@ __global__ __launch_bounds__(kThreads, DW ? 3 : 4) void qk_backward_kernel(QKArg
   const int k = W > 1 ? wave : 0, g0 = W > 1 ? 0 : wave;
   const Lane<L, NB> me(a);
   u32x4 w[2];
-  float dw[2][8];
+  float unit[2], dw[2][8];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     w[i] = me.in && a.heads[i] ? ld16(a.w[i] + 8 * me.chunk) : zero16();
+    unit[i] = 1.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
   }
@@ -269,6 +292,10 @@ __global__ __launch_bounds__(kThreads, DW ? 3 : 4) void qk_backward_kernel(QKArg
     load(0, g0, x[0], d[0]);
     load(1, g0, x[1], d[1]);
     make_turns(a, token0, turns[buf]);
+    if (token0 == (int)blockIdx.x * W) {  // (behind the first loads)
+      unit[0] = weight_unit(w[0]);
+      unit[1] = weight_unit(w[1]);
+    }
     __syncthreads();
     if (!there) continue;
     float c[8], s[8];
@@ -306,8 +333,17 @@ __global__ __launch_bounds__(kThreads, DW ? 3 : 4) void qk_backward_kernel(QKArg
           along += mw[e] * f[e];
         }
         along = sum_over<L>(along) * a.mean;
+        const float outer = r * down;
+        if (unit[kind] == 1.f) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mw[e] = (mw[e] - f[e] * along) * r * down;
+          for (int e = 0; e < 8; ++e) mw[e] = (mw[e] - f[e] * along) * outer;
+        } else {
+          // first the two factors that go opposite ways
+          const bool apart = (outer < 1.f) != (unit[kind] < 1.f);
+          const float y0 = apart ? outer * unit[kind] : outer, y1 = apart ? 1.f : unit[kind];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mw[e] = (mw[e] - f[e] * along) * y0 * y1;
+        }
         const int head = g * H + me.head;
         if (me.in && head < a.heads[kind])
           st_row<NT>(a.o[kind] + (int64_t)token * a.ldo[kind] + (int64_t)head * a.dim + 8 * me.chunk, pack8(mw));
@@ -417,8 +453,9 @@ int check_heads(const lora_qk_heads_t* h) {
   if (h->head_dim > 256) return set_error(LORA_UNSUPPORTED, "head_dim %d is above 256", h->head_dim);
   if (h->rot_dim < 0 || h->rot_dim > h->head_dim || (h->rot_dim & 15))
     return set_error(LORA_INVALID_ARGUMENT, "rot_dim (%d) must be a multiple of 16 from 0 to head_dim (%d)", h->rot_dim, h->head_dim);
-  if (!(h->eps >= 1.17549435e-38f) || !(h->eps <= 3.4e38f))
-    return set_error(LORA_INVALID_ARGUMENT, "eps (%g) must be a positive normal number", (double)h->eps);
+  // (the mean and eps together stay in fp32's range: a mean is at most an eighth of it)
+  if (!(h->eps >= 1.17549435e-38f) || !(h->eps <= 1e30f))
+    return set_error(LORA_INVALID_ARGUMENT, "eps (%g) must be a positive normal number of at most 1e30", (double)h->eps);
   if ((h->heads_q && !h->weight_q) || (h->heads_k && !h->weight_k))
     return set_error(LORA_INVALID_ARGUMENT, "the weight of heads that there are is NULL");
   if ((reinterpret_cast<uintptr_t>(h->weight_q) | reinterpret_cast<uintptr_t>(h->weight_k)) & 15u)

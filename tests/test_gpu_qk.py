@@ -203,6 +203,21 @@ def test_sizes_at_the_ends_of_the_type(T, nb):
     c.check_backward(c.backward(dw, ws=L.new_workspace_qk(c.heads, T)), dw)
 
 
+@pytest.mark.parametrize("T", [12, 2050])
+@pytest.mark.parametrize("x,w,g,eps", [(50, 100, 60, 1e-6), (50, 100, -80, 1e30), (60, -60, 100, 1e-6), (-40, 110, -50, 1e-30)])
+@pytest.mark.parametrize("nb", [False, True])
+def test_products_past_the_type_on_the_way(T, x, w, g, eps, nb):
+    """Values, weights and gradients (powers of two) of which two multiplied leave
+    fp32's range where the results do not; the largest eps."""
+    c = Case(T, 4, 1, 64, 64, nb, eps=eps)
+    c.x, c.gr = ((t.double() * 2.0 ** f).to(torch.bfloat16) for t, f in ((c.x, x), (c.gr, g)))
+    c.w = tuple((v.double() * 2.0 ** w).to(torch.bfloat16) for v in c.w)
+    c.heads = L.QKHeads(4, 1, 64, *c.w, c.freqs, eps=eps, neighbours=nb)
+    c.check_forward(c.forward())
+    dw = torch.empty((2, 64), device="cuda")
+    c.check_backward(c.backward(dw, ws=L.new_workspace_qk(c.heads, T)), dw)
+
+
 @pytest.mark.parametrize("T", [30, 2050])
 def test_not_finite_stays_in_its_head(T):
     c = Case(T, 5, 2, 64, 32)

@@ -52,7 +52,7 @@ def test_struct_matches_the_c_header(tmp_path):
     (dict(hq=-1), "heads_q", 1), (dict(hk=-1), "heads_k", 1), (dict(hq=0, hk=0), "both 0", 1), (dict(hq=65537), "65536", 2),
     (dict(dim=0), "head_dim", 1), (dict(dim=60), "head_dim", 1), (dict(dim=264, rot=64), "256", 2), (dict(rot=-16), "rot_dim", 1),
     (dict(rot=80), "rot_dim", 1), (dict(rot=24), "rot_dim", 1), (dict(eps=0.0), "eps", 1), (dict(eps=-1.0), "eps", 1),
-    (dict(eps=float("nan")), "eps", 1), (dict(eps=float("inf")), "eps", 1), (dict(eps=1e-39), "eps", 1),
+    (dict(eps=float("nan")), "eps", 1), (dict(eps=float("inf")), "eps", 1), (dict(eps=1e-39), "eps", 1), (dict(eps=2e30), "eps", 1),
     (dict(wq=0), "weight", 1), (dict(wk=0), "weight", 1), (dict(wq=A[8] + 8), "aligned", 1), (dict(f=0), "freqs", 1),
     (dict(f=A[10] + 4), "freqs", 1)])
 def test_every_entry_refuses_bad_heads(bad, word, want):
