@@ -227,7 +227,7 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
   const uint64_t xebase = reinterpret_cast<uint64_t>(a.xe) + (uint64_t)t0 * (X8 ? (uint64_t)a.ldxe : 4u);
   to.x = X8 ? xbase : xbase + (uint64_t)k0 * a.ldx;
   to.xbytes = X8 ? (int32_t)((int64_t)(vt - 1) * a.ldx + (int64_t)a.nkb * 128) : vt * 64;
-  to.xat = (uint32_t)k0 * 128u;
+  to.xat = k0 < k1 ? (uint32_t)k0 * 128u : 0u;
 #pragma unroll
   for (int p = 0; p < C::eloads; ++p) {
     const int q = p * C::waves + wave;
@@ -241,13 +241,15 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
   to.left = k1 - k0;
   // Load p of the panel; behind the group's last one the descriptors are empty and
   // the loads write zeros, so that every step issues (and waits for) the same
-  // number without a branch between them.
+  // number without a branch between them. An empty descriptor needs a scalar offset of
+  // 0: the range of a load ends at its bytes less that offset, which must not pass
+  // below 0.
   auto load = [&](int p) {
     const bool live = to.left > 0;
     if (p < C::vloads) {
       const int32_t bytes = isx[p] ? to.xbytes : to.wbytes;
       load_piece16(rsrc_words(isx[p] ? to.x : to.w, live && !none[p] ? bytes : 0), to.at + (p * C::waves + wave) * 1024, vv[p],
-                   X8 && isx[p] ? to.xat : 0);
+                   X8 && isx[p] && !none[p] ? to.xat : 0);
     } else {
       const int q = p - C::vloads;
       load_piece4(rsrc_words(to.e[q], live ? to.ebytes[q] : 0), to.at + C::eoff + (q * C::waves + wave) * 256, ev[q]);
@@ -255,7 +257,7 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
   };
   auto next_panel = [&] {
     to.w += (uint64_t)a.ldw;
-    if constexpr (X8) to.xat += 128u;
+    if constexpr (X8) to.xat = to.left > 1 ? to.xat + 128u : 0u;
     else to.x += (uint64_t)a.ldx;
 #pragma unroll
     for (int p = 0; p < C::eloads; ++p) to.e[p] += to.estep[p];

@@ -213,12 +213,14 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q8_tile_kernel(MatArgs 
   const uint32_t ring0 = lds0 + (uint32_t)(grp * C::ring);
   // Load p of block kb; behind the group's last one the descriptors are empty and the
   // loads write zeros, so that every step issues (and waits for) the same
-  // number without a branch between them.
+  // number without a branch between them. An empty descriptor needs a scalar offset of
+  // 0: the range of a load ends at its bytes less that offset, which must not pass
+  // below 0.
   auto load = [&](int kb, int slot, int p) {
     const int piece = p * C::waves + wave;
     i32x4 r = p >= C::wloads ? xr : wr;
     r[2] = kb < k1 ? r[2] : 0;
-    load_lds16_at(r, ring0 + (uint32_t)(slot * C::stage + piece * 1024), voff[p], (uint32_t)kb * 128u);
+    load_lds16_at(r, ring0 + (uint32_t)(slot * C::stage + piece * 1024), voff[p], kb < k1 ? (uint32_t)kb * 128u : 0u);
   };
 
   const int eb0 = n0 >> 7, vb = ((n0 + vn - 1) >> 7) - eb0 + 1;
