@@ -151,6 +151,7 @@ __device__ __forceinline__ void st_row(uint16_t* p, u32x4 v) {
 // sum(x^2) past fp32's range: x is taken 2^-80 as large (its norm does not change).
 __device__ __forceinline__ bool past_range(float ss) { return !(ss < __builtin_inff()); }
 constexpr float kDown = 0x1p-80f;
+constexpr int kDownPlaces = -80;
 
 // A workgroup takes W tokens: one for each wave (W = 4), or one whose groups of heads
 // the waves take in turn. U groups are loaded before the first is used. Bound by
@@ -230,26 +231,49 @@ __global__ __launch_bounds__(kThreads, 4) void qk_forward_kernel(QKArgs a) {
   heads_of(std::integral_constant<int, 1>{});
 }
 
-// Weights whose largest is 2^32 and more, or below 2^-32, are taken in a unit of their own,
-// a power of two, so that their products with gradients stay in range: brings w
-// to it and returns it (1 for all others, and where one is no number).
-__device__ __forceinline__ float weight_unit(u32x4& w) {
-  uint32_t m = 0;
+// The largest magnitude of 8 bf16, as its bits.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t largest(u32x4 v) {
+  u16x2 m = {0, 0};
 #pragma unroll
-  for (int q = 0; q < 4; ++q) m = max(max(m, (w[q] << 16) & 0x7fffffffu), w[q] & 0x7fff0000u);
-  constexpr uint32_t low = (127u - 32) << 23, high = (127u + 32) << 23;
-  if (__any(m >= low) && !__any(m >= high)) return 1.f;
+  for (int q = 0; q < 4; ++q) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[q] & 0x7fff7fffu));
+  return max((uint32_t)m[0], (uint32_t)m[1]);
+}
+
+// The gradient multiplies gradients by weights by r, whose product can be in range where
+// two of them are not. Weights and gradients are taken as they are while the largest of
+// either is within kWindow binary places of 1; otherwise in units of their own, the power
+// of two of the largest (of the weights, of a head's gradients), and the result gets
+// the units' exponents with r's in one step. So a column of dx is right to its rounding, and to
+// 2^-50 of what the head's largest gradient and largest weight give (2^-64 2^-32 is 2^54
+// times the smallest fp32 number).
+constexpr int kWeightWindow = 32, kGradWindow = 64;
+template <int WINDOW>
+__device__ __forceinline__ bool outside(uint32_t top) {  // (of a magnitude's bits; 0 is inside)
+  constexpr uint32_t low = (127u - WINDOW) << 7, high = (127u + WINDOW) << 7;
+  return top - low >= high - low && top != 0;
+}
+// Exponent of the unit for the largest magnitude's bits: its own, as far as its power and the
+// reciprocal are normal numbers; 0 where it is no number.
+__device__ __forceinline__ int unit_of(uint32_t top) {
+  const int e = (int)(top >> 7);
+  return e == 255 ? 0 : min(max(e, 1), 253) - 127;
+}
+__device__ __forceinline__ float power(int e) { return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23); }
+
+// Brings weights to their unit and returns its exponent.
+__device__ __forceinline__ int weight_unit(u32x4& w) {
+  uint32_t top = largest(w);
+  if (!__any(outside<kWeightWindow>(top))) return 0;
 #pragma unroll
-  for (int l = 1; l < 64; l *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, l));
-  const uint32_t e = __builtin_amdgcn_readfirstlane(m) >> 23;
-  if (e == 0 || e == 255) return 1.f;
-  const uint32_t u = min(e, 253u);
+  for (int l = 1; l < 64; l *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, l));
+  const int u = unit_of(__builtin_amdgcn_readfirstlane(top));
   float f[8];
   unpack8(w, f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] *= __builtin_bit_cast(float, (254u - u) << 23);
+  for (int i = 0; i < 8; ++i) f[i] *= power(-u);
   w = pack8(f);
-  return __builtin_bit_cast(float, u << 23);
+  return u;
 }
 
 // The gradient. The grid is bounded and its workgroups take the tokens in turn, so
@@ -269,11 +293,12 @@ __global__ __launch_bounds__(kThreads, DW ? 3 : 4) void qk_backward_kernel(QKArg
   const int k = W > 1 ? wave : 0, g0 = W > 1 ? 0 : wave;
   const Lane<L, NB> me(a);
   u32x4 w[2];
-  float unit[2], dw[2][8];
+  int unit[2];
+  float dw[2][8];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     w[i] = me.in && a.heads[i] ? ld16(a.w[i] + 8 * me.chunk) : zero16();
-    unit[i] = 1.f;
+    unit[i] = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
   }
@@ -310,6 +335,16 @@ __global__ __launch_bounds__(kThreads, DW ? 3 : 4) void qk_backward_kernel(QKArg
         unpack8(d[kind], m);
         unpack8(w[kind], wf);
         me.pairs(d[kind], m, p);
+        int gu = 0;
+        const bool far = __any(outside<kGradWindow>(largest(d[kind])));
+        if (far) {
+          uint32_t top = largest(d[kind]);
+#pragma unroll
+          for (int l = 1; l < L; l *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, l));
+          gu = unit_of(top);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m[e] *= power(-gu), p[e] *= power(-gu);
+        }
         float ss = 0.f, along = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
@@ -328,21 +363,23 @@ __global__ __launch_bounds__(kThreads, DW ? 3 : 4) void qk_backward_kernel(QKArg
         for (int e = 0; e < 8; ++e) {
           mw[e] = m[e] * c[e] - p[e] * s[e];  // turned back
           f[e] *= r;                          // x / rms
-          if constexpr (DW) dw[kind][e] += mw[e] * f[e];
+          if constexpr (DW) {
+            if (far) dw[kind][e] += __builtin_ldexpf(mw[e] * f[e], gu);
+            else dw[kind][e] += mw[e] * f[e];
+          }
           mw[e] *= wf[e];
           along += mw[e] * f[e];
         }
         along = sum_over<L>(along) * a.mean;
-        const float outer = r * down;
-        if (unit[kind] == 1.f) {
+        if (!far && unit[kind] == 0) {
+          const float outer = r * down;
 #pragma unroll
           for (int e = 0; e < 8; ++e) mw[e] = (mw[e] - f[e] * along) * outer;
         } else {
-          // first the two factors that go opposite ways
-          const bool apart = (outer < 1.f) != (unit[kind] < 1.f);
-          const float y0 = apart ? outer * unit[kind] : outer, y1 = apart ? 1.f : unit[kind];
+          const float fraction = __builtin_amdgcn_frexp_mantf(r);
+          const int places = __builtin_amdgcn_frexp_expf(r) + (down == 1.f ? 0 : kDownPlaces) + gu + unit[kind];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) mw[e] = (mw[e] - f[e] * along) * y0 * y1;
+          for (int e = 0; e < 8; ++e) mw[e] = __builtin_ldexpf((mw[e] - f[e] * along) * fraction, places);
         }
         const int head = g * H + me.head;
         if (me.in && head < a.heads[kind])
