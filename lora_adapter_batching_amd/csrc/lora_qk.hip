@@ -96,23 +96,24 @@ __device__ __forceinline__ u32x4 from_lane(u32x4 v, int lane) {
 template <int L, bool NB>
 struct Lane {
   int chunk, head, other;
-  bool in, turned, upper;
+  bool in, turned, upper, part;
   __device__ __forceinline__ explicit Lane(const QKArgs& a) {
     const int lane = threadIdx.x & 63;
     chunk = lane & (L - 1);
     head = lane / L;
     in = 8 * chunk < a.dim;
     turned = 8 * chunk < a.rot;
+    part = a.rot < a.dim;
     const int h = a.rot >> 4;  // chunks of half the turned columns
     upper = chunk >= h;
     other = NB || !turned ? lane : upper ? lane - h : lane + h;
   }
   // The rotation of its columns: column e becomes c[e] times itself plus s[e] times
-  // its pair's other member.
+  // its pair's other member (-0 times it where there is none, which leaves any sum as it is).
   template <int W>
   __device__ __forceinline__ void turn(const QKArgs& a, const Turns<W>& t, int k, float (&c)[8], float (&s)[8]) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = 0.f;
+    for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = -0.f;
     if (!turned) return;
     if constexpr (NB) {
       const f32x4 vc = *reinterpret_cast<const f32x4*>(&t.c[k][4 * chunk]), vs = *reinterpret_cast<const f32x4*>(&t.s[k][4 * chunk]);
@@ -124,13 +125,18 @@ struct Lane {
       for (int e = 0; e < 8; ++e) c[e] = t.c[k][first + e], s[e] = upper ? t.s[k][first + e] : -t.s[k][first + e];
     }
   }
-  // The other members of its pairs.
+  // The other members of its pairs; 0 for columns without one, whose neighbours may hold
+  // anything (0 times an infinity or NaN is NaN).
   __device__ __forceinline__ void pairs(u32x4 v, const float (&f)[8], float (&p)[8]) const {
     if constexpr (NB) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) p[e] = f[e ^ 1];
     } else {
       unpack8(from_lane(v, other), p);
+    }
+    if (part) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = turned ? p[e] : 0.f;
     }
   }
 };
