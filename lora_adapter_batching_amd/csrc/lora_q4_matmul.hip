@@ -171,7 +171,8 @@ struct Tile4 {
   static constexpr int lds = used > epi ? used : epi;
   static_assert(!X8 || BT % (8 * waves) == 0, "whole exponent loads");
   static_assert(TT % 32 == 0 && TN % 32 == 0, "whole fragments");
-  static_assert(S >= 2 && lds <= 160 * 1024 && (S - 1) * loads < 64, "fits the LDS and the load counter");
+  static_assert(S >= 3, "with two stages the loads of half 0 would be waited for at once");
+  static_assert(lds <= 160 * 1024 && (S - 1) * loads < 64, "fits the LDS and the load counter");
 };
 
 // Exponents of 8-bit rows in LDS: rows of 8 dwords of four blocks each, dword d of
@@ -339,7 +340,7 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
   // others in half 0 of step i + 1.
   constexpr int M = C::FT * C::FN, F = C::FN + C::FT;
   constexpr int early = (F + (M > 1 ? M / 2 : 1) - 1) / (M > 1 ? M / 2 : 1);
-  constexpr int ahead = C::S == 2 ? C::loads : C::loads / 2;  // loads of half 1 (two stages: those of half 0 would be waited for at once)
+  constexpr int ahead = C::loads / 2;  // loads of half 1
   auto half = [&](auto sc, const Exps& e, int at, int nx, int kb, int kb0, Exps& raw) {
     constexpr int s = decltype(sc)::value;
 #pragma unroll
