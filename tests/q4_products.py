@@ -17,3 +17,17 @@ PRODUCTS = [
     (4, 35, 1584, 4136), (8, 35, 1584, 4136), (8, 36, 14504, 4168),         # 32 x 64, in four
     (4, 35, 2168, 40), (8, 35, 2168, 40), (8, 33, 14440, 40),               # 32 x 32, in four
 ]
+
+# Sums so long that a workgroup fetches the exponents of 8-bit rows three times, for every tile.
+LONG_SUMS = [
+    (8, 1795, 7400, 5456),      # 256 x 256
+    (8, 385, 7400, 11016),      # 256 x 128
+    (8, 257, 7400, 11704),      # 128 x 160
+    (8, 130, 7400, 14824),      # 128 x 128
+    (8, 137, 7400, 11896),      # 128 x 96
+    (8, 66, 7400, 13384),       # 64 x 64
+    (8, 65, 15000, 8528),       # 64 x 96, the sum in two parts
+    (8, 65, 29000, 6040),       # 64 x 64, in four
+    (8, 36, 29000, 4168),       # 32 x 64, in four
+    (8, 33, 29000, 40),         # 32 x 32, in four
+]

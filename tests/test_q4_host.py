@@ -14,7 +14,7 @@ import torch
 import lora_adapter_batching_amd as L
 from lora_adapter_batching_amd import binding as B
 from tests import q4_ref as R
-from tests.q4_products import PRODUCTS
+from tests.q4_products import LONG_SUMS, PRODUCTS
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P, D = 1 << 40, 1 << 41  # aligned stand-in addresses, never read
@@ -230,3 +230,13 @@ def test_matmul_inspection_refusals():
     for args in [(4, 0, 8, 8, by(out)), (4, 1, 0, 8, by(out)), (8, 1, 8, 0, by(out)), (4, 1, 12, 8, by(out)), (4, 1, 8, 12, by(out)),
                  (4, 1, 8, 8, None), (16, 1, 8, 8, by(out))]:
         assert lib.lora_inspect_matmul4(*args) == B.LORA_INVALID_ARGUMENT
+
+
+def test_long_sums_fetch_their_exponents_three_times():
+    """The long sums that the GPU tests multiply take every tile, each past two refills of its staged exponents."""
+    chosen = {}
+    for bits, T, K, N in LONG_SUMS:
+        k = B.inspect_matmul4(bits, T, K, N)
+        assert bits == 8 and (k.blocks - 1) // k.exps >= 2, (T, K, N)
+        chosen[k.kernel] = k
+    assert sorted(chosen) == list(range(1, k.kernels))
