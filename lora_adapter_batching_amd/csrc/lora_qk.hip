@@ -501,7 +501,7 @@ int check_heads(const lora_qk_heads_t* h) {
     return set_error(LORA_INVALID_ARGUMENT, "eps (%g) must be a positive normal number of at most 1e30", (double)h->eps);
   if ((h->heads_q && !h->weight_q) || (h->heads_k && !h->weight_k))
     return set_error(LORA_INVALID_ARGUMENT, "the weight of heads that there are is NULL");
-  if ((reinterpret_cast<uintptr_t>(h->weight_q) | reinterpret_cast<uintptr_t>(h->weight_k)) & 15u)
+  if ((h->heads_q && (reinterpret_cast<uintptr_t>(h->weight_q) & 15u)) || (h->heads_k && (reinterpret_cast<uintptr_t>(h->weight_k) & 15u)))
     return set_error(LORA_INVALID_ARGUMENT, "a weight is not 16-byte aligned");
   if (h->rot_dim && (!h->freqs || (reinterpret_cast<uintptr_t>(h->freqs) & 7u)))
     return set_error(LORA_INVALID_ARGUMENT, "freqs is NULL or not 8-byte aligned");

@@ -166,3 +166,13 @@ def test_reference_gradient_against_autograd_and_differences(neighbours):
     # a rotation keeps lengths, and position 0 turns nothing
     n = x.detach() / torch.sqrt((x.detach() ** 2).mean(-1, keepdim=True) + 1e-3) * w.detach()
     assert torch.allclose(out.detach().norm(dim=-1), n.norm(dim=-1)) and torch.allclose(out.detach()[0], n[0])
+
+
+def test_the_weight_of_no_heads_is_ignored():
+    """At any address (what is refused is something else, behind that check)."""
+    st, msg = forward(heads(hk=0, wk=A[9] + 2), k=(0, 0), ko=(0, 0), qo=(A[2], 248))
+    assert st == 1 and "q_out" in msg
+    st, msg = backward(heads(hq=0, wq=A[8] + 2), q=(0, 0), gq=(0, 0), dq=(0, 0), flags=4)
+    assert st == 1 and "flags" in msg
+    st, msg = forward(heads(hk=0, wq=A[8] + 2, wk=0), k=(0, 0), ko=(0, 0))
+    assert st == 1 and "aligned" in msg
