@@ -527,8 +527,8 @@ typedef struct lora_qk_heads_t {
 
 /*
  * positions: DEVICE int32 [num_tokens]. q_out / k_out may be q / k themselves
- * (the same address and stride); otherwise the buffers must not overlap. Can
- * be captured into a HIP graph.
+ * (the same address, and the same stride if there is more than one token);
+ * otherwise the buffers must not overlap. Can be captured into a HIP graph.
  */
 int lora_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, const lora_qk_heads_t* heads,
                       const int32_t* positions, int32_t num_tokens, void* q_out, int64_t ldqo, void* k_out,

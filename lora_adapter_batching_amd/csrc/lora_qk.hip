@@ -569,7 +569,7 @@ extern "C" int lora_qk_norm_rope(const void* q, int64_t ldq, const void* k, int6
   const bool both = heads->heads_q && heads->heads_k;
   if (both && (q_out == k_out || q_out == k || k_out == q))
     return set_error(LORA_INVALID_ARGUMENT, "an output starts at the other output or at the other input");
-  if ((heads->heads_q && q_out == q && ldqo != ldq) || (heads->heads_k && k_out == k && ldko != ldk))
+  if (num_tokens > 1 && ((heads->heads_q && q_out == q && ldqo != ldq) || (heads->heads_k && k_out == k && ldko != ldk)))
     return set_error(LORA_INVALID_ARGUMENT, "an output that takes its input's place needs its row stride");
   QKArgs a = args_of(heads, q, ldq, k, ldk, positions, num_tokens, q_out, ldqo, k_out, ldko);
   const hipStream_t s = static_cast<hipStream_t>(stream);

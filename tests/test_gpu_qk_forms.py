@@ -25,3 +25,14 @@ def test_batches_past_the_caches(T, hq, hk, D, rot, nb):
     back = c.backward(dw, ws=L.new_workspace_qk(c.heads, T))
     c.check_backward(back, dw)
     assert torch.equal(back, c.backward())
+
+
+def test_one_token_in_place_of_many_rows():
+    """A single token's row has no stride: an output of one row takes the place of the first of several."""
+    c = Case(1, 3, 2, 64, 64)
+    want = c.forward()
+    q, k = c.x[:, 8:8 + 192], c.x[:, 200:200 + 128]
+    assert q.shape[0] == 2
+    rest = c.x[1].clone()
+    L.qk_norm_rope(q, k, c.heads, c.pos, q[:1], k[:1])
+    assert torch.equal(q[:1], c.cols(want, 0)) and torch.equal(k[:1], c.cols(want, 1)) and torch.equal(c.x[1], rest)
