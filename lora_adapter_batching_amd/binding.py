@@ -644,10 +644,10 @@ def new_q4(rows: int, width: int, device="cuda") -> Q4:
     return Q4(v, e, width)
 
 
-def _q4_arg(name: str, q, dev: int) -> int:
+def _q4_arg(name: str, q, dev: Optional[int] = None) -> int:
     if type(q) is not Q4:
         raise ValueError(f"{name} must be a Q4, got {type(q).__name__}")
-    if q.dev != dev:
+    if dev is not None and q.dev != dev:
         raise ValueError(f"{name} is on {_dev_name(q.dev)}, expected {_dev_name(dev)}")
     return q.addr4
 
@@ -655,8 +655,8 @@ def _q4_arg(name: str, q, dev: int) -> int:
 def q4_quantize(x, out: Q4, out_t: Optional[Q4] = None, stream=None):
     """Stores bf16 x in 4 bits; with out_t the transposed matrix too, scales
     then shared by 32 x 32 values so that both hold the same numbers."""
-    lib, dev = _lib or load(), out.dev
-    o = _q4_arg("out", out, dev)
+    lib, o = _lib or load(), _q4_arg("out", out)
+    dev = out.dev
     ldx = _rows_arg("x", x, out.rows, out.width, dev)
     ot = _q4_arg("out_t", out_t, dev) if out_t is not None else None
     _call_on(dev, stream, lib.lora_q4_quantize, x.data_ptr(), ldx, o, ot)
@@ -664,8 +664,7 @@ def q4_quantize(x, out: Q4, out_t: Optional[Q4] = None, stream=None):
 
 def q4_dequantize(q: Q4, x, stream=None):
     """Restores a 4-bit matrix to bf16 x."""
-    lib = _lib or load()
-    a = _q4_arg("q", q, q.dev)
+    lib, a = _lib or load(), _q4_arg("q", q)
     ldx = _rows_arg("x", x, q.rows, q.width, q.dev)
     _call_on(q.dev, stream, lib.lora_q4_dequantize, a, x.data_ptr(), ldx)
 
@@ -673,12 +672,13 @@ def q4_dequantize(q: Q4, x, stream=None):
 def q4_matmul(x, w: Q4, y, accumulate: bool = False, stream=None):
     """y = x w^T (or y += x w^T) on 4-bit weights; x in 4 bits (Q4) or 8-bit
     rows (Q8Rows); y bf16 [x.rows, w.rows]."""
-    lib, dev = _lib or load(), x.dev
-    wa = _q4_arg("w", w, dev)
+    lib = _lib or load()
     if type(x) is Q8Rows:
         fn, xa = lib.lora_q4_matmul_q8, x.addr
     else:
-        fn, xa = lib.lora_q4_matmul, _q4_arg("x (Q4 or Q8Rows)", x, dev)
+        fn, xa = lib.lora_q4_matmul, _q4_arg("x (Q4 or Q8Rows)", x)
+    dev = x.dev
+    wa = _q4_arg("w", w, dev)
     ldy = _rows_arg("y", y, x.rows, w.rows, dev)
     _call_on(dev, stream, fn, xa, wa, y.data_ptr(), ldy, 1 if accumulate else 0)
 

@@ -240,3 +240,11 @@ def test_long_sums_fetch_their_exponents_three_times():
         assert bits == 8 and (k.blocks - 1) // k.exps >= 2, (T, K, N)
         chosen[k.kernel] = k
     assert sorted(chosen) == list(range(1, k.kernels))
+
+
+def test_binding_names_what_is_no_store():
+    q, x = L.new_q4(4, 128, device="cpu"), torch.zeros((4, 128), dtype=torch.bfloat16)
+    for call in (lambda: L.q4_quantize(x, x), lambda: L.q4_quantize(x, None), lambda: L.q4_quantize(x, q, x), lambda: L.q4_dequantize(x, x),
+                 lambda: L.q4_matmul(x, q, x), lambda: L.q4_matmul(q, x, x), lambda: L.q4_matmul(None, q, x)):
+        with pytest.raises(ValueError, match="must be a Q4"):
+            call()
