@@ -8,6 +8,15 @@
 // as they are. With both operands in 4 bits it runs at twice the rate of the
 // 8-bit forms; 8-bit rows on 4-bit weights run at the 8-bit rate and read half
 // the weights' bytes.
+//
+// Precision. The accumulators are fp32. Products of two e2m1 values are whole
+// multiples of 1/4 up to 36, and their sums inside a block of 32 are exact. With 8-bit
+// rows the instruction first adds eight neighbouring products on a grid of 2^-13 of the
+// largest one's power of two (2^8 + 2^-5 - 2^8 in a group of eight gives 2^-5, with 2^-6 it
+// gives 0; the third value in the next group: 2^-6), about 2e-5 of the result on normal
+// inputs, which moves one bf16 result in a hundred by a step. The e4m3 rounding of the
+// rows is 2^-4 a value and the result's 2^-8, so it is kept: bf16 products of the same
+// values would be exact in fp32 at half the matrix rate and an expansion of every fragment.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -509,7 +518,8 @@ __global__ __launch_bounds__(64 * C::waves * C::KS) void q4_tile_kernel(Mat4Args
 // 1 KB) and their parts are added in wave order. 1 token (8-bit x), us: 2560 -> 2560 2.8,
 // which is one launch, 2560 -> 19456 6.4 (4.1 TB/s), 9728 -> 2560 5.8 (ten panels a
 // wave, one behind the other). Two to four panels in flight a wave or 16 waves were
-// slower (6.4 -> 7.1-9.4 for 2560 -> 19456).
+// slower where 1216 workgroups fill the GPU (6.4 -> 7.1-9.4 for 2560 -> 19456); with 160
+// of them (2560 columns) that was not measured.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
 constexpr int kFewTokens = 16;
@@ -586,7 +596,8 @@ void launch_few(const Mat4Args& a, bool add, hipStream_t s) {
 // Tiles to choose from. A workgroup of a tile takes about fixed + step * (its
 // panels of the sum) microseconds while `slots` of them run, so a product takes
 // that times the rounds its tiles need: a fit to these times on 256 CUs (us, 8-bit x /
-// 4-bit x; tiles are tokens x columns, :n the groups of waves that share the sum).
+// 4-bit x; tiles are tokens x columns, :n the groups of waves that share the sum), of calls
+// repeated on the same operands, which the caches then hold.
 //   37, 2560, 2560       64x64 7.1/5.8    64x96:2 7.1/6.5   64x64:4 6.6/5.5    32x64:4 5.0/4.5    32x32:4 4.4/3.9
 //   37, 9728, 2560       64x64 20.1/15.2  64x96:2 16.1/14.6 64x64:4 13.0/10.2  32x64:4 9.9/8.7    32x32:4 8.0/6.5
 //   100, 9728, 2560      64x64 20.1/15.3  64x96:2 16.7/14.7 64x64:4 13.6/10.3  32x64:4 10.2/8.8   32x32:4 14.0/9.2
@@ -599,7 +610,8 @@ void launch_few(const Mat4Args& a, bool add, hipStream_t s) {
 //   8191, 4096, 4096     256x256 94/69    256x128 117/75    128x128 115/80
 //   8192, 4096, 14336    256x256 324/236  256x128 398/249   128x128 386/276
 // Over the 34 products it is made from, the choice is the fastest tile of the list or within
-// 7% of it. Nothing in it stands for the weights' bytes. (128x160 has four stages: with its
+// 7% of it, for operands in the caches. Nothing in it stands for the weights' bytes: on
+// weights from memory, as a model's layers bring them, it was not fitted. (128x160 has four stages: with its
 // operands from memory 256, 2560, 19456 takes 17.3/14.1, with three 18.0/15.4, with five 17.7/14.5.)
 struct TileChoice {
   int bt, bn, ks, stages, slots;
