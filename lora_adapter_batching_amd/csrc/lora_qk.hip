@@ -131,12 +131,14 @@ struct Lane {
     if constexpr (NB) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) p[e] = f[e ^ 1];
-    } else {
-      unpack8(from_lane(v, other), p);
-    }
-    if (part) {
+      if (part) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = turned ? p[e] : 0.f;
+        for (int e = 0; e < 8; ++e) p[e] = turned ? p[e] : 0.f;
+      }
+    } else {
+      u32x4 o = from_lane(v, other);
+      if (part) o = turned ? o : zero16();
+      unpack8(o, p);
     }
   }
 };
