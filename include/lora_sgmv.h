@@ -512,10 +512,10 @@ int lora_q4_matmul_q8(const lora_q8_t* x, const lora_q4_t* w, void* y, int64_t l
  * unturned. Everything is in fp32 and rounded once to bf16, but for the
  * angles: those are taken in 64 bits and reduced to part of a turn first, so
  * far positions keep their digits. (x r is formed first: where eps is far
- * above mean(x^2) and 1, an x r below 2^-126 keeps fewer digits.) A head's columns follow each other, heads
- * follow each other in a token's row: q is [num_tokens, heads_q * head_dim]
- * with row stride ldq, k alike, both may be columns of one joint matrix. A
- * kind with 0 heads has its pointers ignored.
+ * above mean(x^2) and 1, an x r below 2^-126 keeps fewer digits.) A head's
+ * columns follow each other, heads follow each other in a token's row: q is
+ * [num_tokens, heads_q * head_dim] with row stride ldq, k alike, both may be
+ * columns of one joint matrix. A kind with 0 heads has its pointers ignored.
  */
 typedef struct lora_qk_heads_t {
   int32_t heads_q;      /* 0..65536 */
@@ -548,9 +548,10 @@ int lora_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, co
  * zeros for no tokens). The order of its sums is fixed: the same call gives
  * the same bits. Gradients and weights may have any size as long as dx is in
  * range: a column of dx is right to its rounding in fp32, and to 2^-50 of the
- * head's largest gradient times the largest weight times r. dweight needs a workspace of lora_workspace_size_qk() bytes,
- * 16-byte aligned, in any state; calls that share one must be ordered. The
- * buffers must not overlap. Can be captured into a HIP graph.
+ * head's largest gradient times the largest weight times r. dweight needs a
+ * workspace of lora_workspace_size_qk() bytes, 16-byte aligned, in any state;
+ * calls that share one must be ordered. The buffers must not overlap. Can be
+ * captured into a HIP graph.
  */
 int lora_workspace_size_qk(const lora_qk_heads_t* heads, int32_t num_tokens, size_t* bytes);
 int lora_qk_norm_rope_backward(const void* q, int64_t ldq, const void* k, int64_t ldk, const lora_qk_heads_t* heads,

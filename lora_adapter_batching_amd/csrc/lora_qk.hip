@@ -249,11 +249,11 @@ __device__ __forceinline__ uint32_t largest(u32x4 v) {
 }
 
 // The gradient multiplies gradients by weights by r, whose product can be in range where
-// two of them are not. Weights and gradients are taken as they are while the largest of
-// either is within kWindow binary places of 1; otherwise in units of their own, the power
-// of two of the largest (of the weights, of a head's gradients), and the result gets
+// two of them are not. Weights are taken as they are while the largest is within
+// kWeightWindow binary places of 1, gradients while a head's largest is within kGradWindow;
+// otherwise in units of their own, the power of two of that largest, and the result gets
 // the units' exponents with r's in one step. So a column of dx is right to its rounding, and to
-// 2^-50 of what the head's largest gradient and largest weight give (2^-64 2^-32 is 2^54
+// 2^-50 of what the head's largest gradient and largest weight give (2^-64 2^-32 is 2^53
 // times the smallest fp32 number). The look at the gradients costs no time: 16384 tokens,
 // 32 + 8 heads of 128, 98-100 us a pass with dweight, with it and without.
 constexpr int kWeightWindow = 32, kGradWindow = 64;
